@@ -53,7 +53,10 @@ extern "C" {
 #define ATTN_VARLEN_ERR_WORKSPACE_SMALL   -8  /* caller workspace below the minimum */
 #define ATTN_VARLEN_ERR_DRIVER            -9  /* tensor-map encoder unavailable     */
 #define ATTN_VARLEN_ERR_NOALLOC_LIMIT    -10  /* num_seqs above the fixed scratch   */
-#define ATTN_VARLEN_ERR_BAD_BLOCK_TABLE  -11  /* paged decode: block id out of range */
+#define ATTN_VARLEN_ERR_BAD_BLOCK_TABLE  -11  /* paged cache: block id out of range */
+#define ATTN_VARLEN_ERR_BAD_DRAFT        -12  /* paged cache: parent or draft index */
+#define ATTN_VARLEN_ERR_NO_FREE_BLOCK    -13  /* paged cache: no page for a fork    */
+#define ATTN_VARLEN_ERR_BAD_ROW          -14  /* paged cache: row index or count    */
 
 /*
  * attn_varlen_fwd -- the attention forward described above.
@@ -158,7 +161,8 @@ int attn_varlen_fwd_ws(const void* q, const void* k, const void* v,
  * word of the current device's library-owned workspace.  Returns
  * ATTN_VARLEN_OK, ATTN_VARLEN_ERR_DEVICE_TIMEOUT when a kernel wait ran out of
  * time since the last check, or ATTN_VARLEN_ERR_CUDA when the stream reports
- * an error.
+ * an error.  Also reads and clears the paged operators' status on the device
+ * (ATTN_VARLEN_ERR_BAD_BLOCK_TABLE, _BAD_DRAFT, _NO_FREE_BLOCK, _BAD_ROW).
  */
 int attn_varlen_check(cudaStream_t stream);
 

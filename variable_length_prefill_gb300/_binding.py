@@ -24,10 +24,13 @@ ERR_WORKSPACE_SMALL = -8
 ERR_DRIVER = -9
 ERR_NOALLOC_LIMIT = -10
 ERR_BAD_BLOCK_TABLE = -11
+ERR_BAD_DRAFT = -12
+ERR_NO_FREE_BLOCK = -13
+ERR_BAD_ROW = -14
 NOALLOC_MAX_SEQS = 1024
 
 # Every symbol the header declares, with (restype, argtypes).
-_P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _SZ, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
 SYMBOLS = {
     "attn_varlen_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P]),
     "attn_varlen_workspace_size": (_SZ, [_I]),
@@ -44,6 +47,13 @@ SYMBOLS = {
     "paged_attn_decode": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
     "chunk_delta_rule_output": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
                                      ctypes.c_float, _P, _P]),
+    "paged_attn_cache_write": (_I, [_P] * 7 + [_I] * 7 + [_L] * 4 + [_P]),
+    "paged_attn_cache_accept": (_I, [_P] * 7 + [_I] * 7 + [_P, _P]),
+    "paged_attn_cache_free": (_I, [_P] * 4 + [_I] * 5 + [_P]),
+    "paged_attn_cache_fork_workspace_size": (_SZ, [_I, _I]),
+    "paged_attn_cache_fork": (_I, [_P] * 7 + [_I] * 7 + [_P, _SZ, _P]),
+    "paged_attn_cache_compact_workspace_size": (_SZ, [_I]),
+    "paged_attn_cache_compact": (_I, [_P] * 5 + [_I] * 6 + [_P, _P, _P, _SZ, _P]),
 }
 
 _LOCK = threading.Lock()
@@ -266,3 +276,195 @@ def chunk_delta_rule_output(q, k, v, h, g, chunk_size=64, scale=None, out=None, 
     if rc != OK:
         raise AttnVarlenError(rc, "chunk_delta_rule_output")
     return out
+
+
+# ------------------------------------------------------------- paged cache
+# The operators below share their checks: every array on the first tensor's
+# device, int32 arrays contiguous, the two caches of one shape family.
+def _int32(device, **arrays):
+    import torch
+    for name, (t, shape) in arrays.items():
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != device \
+                or tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
+
+
+def _cache(k_cache, v_cache):
+    """(num_blocks, num_kv_heads, head_size, block_size) of a pair of caches."""
+    import torch
+    if k_cache.dim() != 5 or v_cache.dim() != 4:
+        raise ValueError("k_cache [B, Hkv, D/8, bs, 8], v_cache [B, Hkv, D, bs]")
+    nb, hkv, d, bs = v_cache.shape
+    if tuple(k_cache.shape) != (nb, hkv, d // 8, bs, 8) or d % 8:
+        raise ValueError(f"k_cache {list(k_cache.shape)} does not fit v_cache {list(v_cache.shape)}")
+    if k_cache.dtype not in (torch.bfloat16, torch.float16) or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must both be bf16 or both fp16")
+    for t in (k_cache, v_cache):
+        if not t.is_cuda or not t.is_contiguous() or t.device != k_cache.device:
+            raise ValueError("k_cache and v_cache must be contiguous tensors on one CUDA device")
+    return nb, hkv, d, bs
+
+
+class _On:
+    """The device of a call, and the stream its work and its allocations go to."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device = torch.cuda.device(device)
+        self.stream = torch.cuda.stream(stream) if stream is not None else None
+        self.where = device
+
+    def __enter__(self):
+        import torch
+        self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return torch.cuda.current_stream(self.where).cuda_stream
+
+    def __exit__(self, *a):
+        if self.stream is not None:
+            self.stream.__exit__(*a)
+        return self.device.__exit__(*a)
+
+
+def _done(rc, where):
+    if rc != OK:
+        raise AttnVarlenError(rc, where)
+
+
+def paged_attn_cache_write(key, value, k_cache, v_cache, block_tables, seq_lens, cu_seqlens,
+                           stream=None):
+    """Write new tokens' keys and values into a paged cache (include/paged_attn_cache.h).
+
+    key, value [total, Hkv, D] of the caches' type, packed by cu_seqlens int32
+    [S + 1]; the head's elements contiguous, token and head strides multiples
+    of 8 (views of a fused projection).  block_tables int32 [S, max_blocks];
+    seq_lens int32 [S] counts the new tokens already: the last n of row i are
+    the ones written.  The caches are changed in place.
+    """
+    nb, hkv, d, bs = _cache(k_cache, v_cache)
+    dev = k_cache.device
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [S, max_blocks]")
+    s, w = block_tables.shape
+    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)),
+           cu_seqlens=(cu_seqlens, (s + 1,)))
+    for name, t in (("key", key), ("value", value)):
+        if t.dtype != k_cache.dtype or t.device != dev or t.dim() != 3 \
+                or tuple(t.shape[1:]) != (hkv, d) or t.shape[0] != key.shape[0] \
+                or (t.stride(2) != 1 and t.numel()):
+            raise ValueError(f"{name} must be {k_cache.dtype} [total, {hkv}, {d}] on {dev} with "
+                             "contiguous head elements")
+    with _On(dev, stream) as h:
+        _done(load().paged_attn_cache_write(
+            key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), s, key.shape[0],
+            hkv, d, bs, w, nb, key.stride(0), key.stride(1), value.stride(0), value.stride(1), h),
+            "paged_attn_cache_write")
+
+
+def paged_attn_cache_accept(k_cache, v_cache, block_tables, seq_lens, cu_seqlens, accepted,
+                            num_accepted, out=None, stream=None):
+    """Move each row's accepted drafts up to the end of its context.
+
+    The last n = cu_seqlens[i + 1] - cu_seqlens[i] tokens of row i are drafts;
+    accepted int32 [S, A] lists the accepted ones in increasing order,
+    num_accepted int32 [S] says how many.  Returns the rows' new lengths
+    (int32 [S], not seq_lens itself).
+    """
+    import torch
+    nb, hkv, d, bs = _cache(k_cache, v_cache)
+    dev = k_cache.device
+    if block_tables.dim() != 2 or accepted.dim() != 2:
+        raise ValueError("block_tables must be [S, max_blocks], accepted [S, A]")
+    s, w = block_tables.shape
+    a = accepted.shape[1]
+    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)),
+           cu_seqlens=(cu_seqlens, (s + 1,)), accepted=(accepted, (s, a)),
+           num_accepted=(num_accepted, (s,)))
+    with _On(dev, stream) as h:
+        if out is None:
+            out = torch.empty_like(seq_lens)
+        _int32(dev, out=(out, (s,)))
+        if s and out.data_ptr() in (seq_lens.data_ptr(), num_accepted.data_ptr()):
+            raise ValueError("out must not be seq_lens or num_accepted")
+        _done(load().paged_attn_cache_accept(
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+            cu_seqlens.data_ptr(), accepted.data_ptr(), num_accepted.data_ptr(), s, a, hkv, d, bs,
+            w, nb, out.data_ptr(), h), "paged_attn_cache_accept")
+    return out
+
+
+def paged_attn_cache_free(block_tables, seq_lens, refs, rows, block_size=16, stream=None):
+    """Rows give their pages back: counts go down by one, seq_lens[rows] = 0.
+
+    refs int32 [num_blocks] counts the rows that hold each page; rows int32
+    [n].  seq_lens and refs are changed in place.
+    """
+    dev = block_tables.device
+    if block_tables.dim() != 2 or rows.dim() != 1 or refs.dim() != 1 or not block_tables.is_cuda:
+        raise ValueError("block_tables [S, max_blocks], refs [num_blocks], rows [n] on a CUDA device")
+    s, w = block_tables.shape
+    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)),
+           refs=(refs, (refs.numel(),)), rows=(rows, (rows.numel(),)))
+    with _On(dev, stream) as h:
+        _done(load().paged_attn_cache_free(block_tables.data_ptr(), seq_lens.data_ptr(),
+                                           refs.data_ptr(), rows.data_ptr(), rows.numel(), s,
+                                           int(block_size), w, refs.numel(), h),
+              "paged_attn_cache_free")
+
+
+def paged_attn_cache_fork(k_cache, v_cache, block_tables, seq_lens, refs, src, dst, stream=None):
+    """Rows dst become copies of rows src: whole pages shared, a partial last
+    page copied into the lowest free page (beams, samples of one prompt).
+
+    src, dst int32 [n]; every dst row is empty, no src and named once.
+    The caches, block_tables, seq_lens and refs are changed in place.
+    """
+    import torch
+    nb, hkv, d, bs = _cache(k_cache, v_cache)
+    dev = k_cache.device
+    if block_tables.dim() != 2 or src.dim() != 1:
+        raise ValueError("block_tables must be [S, max_blocks], src and dst [n]")
+    s, w = block_tables.shape
+    n = src.numel()
+    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)), refs=(refs, (nb,)),
+           src=(src, (n,)), dst=(dst, (n,)))
+    lib = load()
+    size = lib.paged_attn_cache_fork_workspace_size(n, s)
+    with _On(dev, stream) as h:
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        _done(lib.paged_attn_cache_fork(
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+            refs.data_ptr(), src.data_ptr(), dst.data_ptr(), n, s, hkv, d, bs, w, nb,
+            ws.data_ptr(), size, h), "paged_attn_cache_fork")
+
+
+def paged_attn_cache_compact(k_cache, v_cache, block_tables, seq_lens, refs, out=None, stream=None):
+    """Move the used pages (refs > 0) to the lowest ids.
+
+    Returns (block_tables, refs) after the move; ``out``: the pair to write,
+    which may be the inputs themselves (in place).  The caches are changed in
+    place; seq_lens says how many entries of a row are live.
+    """
+    import torch
+    nb, hkv, d, bs = _cache(k_cache, v_cache)
+    dev = k_cache.device
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [S, max_blocks]")
+    s, w = block_tables.shape
+    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)), refs=(refs, (nb,)))
+    if s == 0:
+        raise ValueError("block_tables has no row")
+    lib = load()
+    size = lib.paged_attn_cache_compact_workspace_size(nb)
+    with _On(dev, stream) as h:
+        tables_out, refs_out = out if out is not None else (torch.empty_like(block_tables),
+                                                            torch.empty_like(refs))
+        _int32(dev, out_block_tables=(tables_out, (s, w)), out_refs=(refs_out, (nb,)))
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        _done(lib.paged_attn_cache_compact(
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+            refs.data_ptr(), s, hkv, d, bs, w, nb, tables_out.data_ptr(), refs_out.data_ptr(),
+            ws.data_ptr(), size, h), "paged_attn_cache_compact")
+    return tables_out, refs_out

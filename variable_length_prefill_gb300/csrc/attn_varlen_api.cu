@@ -9,13 +9,16 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "attn_varlen.h"
 #include "attn_varlen_internal.h"
 #include "chunk_delta_rule.h"
 #include "chunk_o_internal.h"
+#include "paged_attn_cache.h"
 #include "paged_attn_decode.h"
+#include "paged_cache_internal.h"
 #include "paged_decode_internal.h"
 
 namespace {
@@ -53,6 +56,10 @@ DeviceState g_dev[kMaxDevices];
 constexpr size_t kNoAllocBytes = avp::ws_layout(ATTN_VARLEN_NOALLOC_MAX_SEQS).total;
 static __device__ __align__(256) unsigned char g_noalloc_scratch[kNoAllocBytes];
 void* g_noalloc_ptr[kMaxDevices] = {};
+// Status word of the paged-cache operators: it never moves, so a captured
+// graph that holds its address stays valid.
+static __device__ int g_page_status;
+int* g_page_status_ptr[kMaxDevices] = {};
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 bool g_encode_probed = false;
 
@@ -283,6 +290,71 @@ int current_device(int* dev) {
   return ATTN_VARLEN_OK;
 }
 
+// Checks shared by the paged-cache operators; OK also where there is nothing
+// to do.
+int check_cache(const void* k_cache, const void* v_cache, int num_kv_heads, int head_size,
+                int block_size, int max_blocks, int num_blocks) {
+  if (num_kv_heads < 1) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (!avp::paged_head_size_supported(head_size)) return ATTN_VARLEN_ERR_UNSUPPORTED_DIM;
+  if (block_size != avp::kPageTokens || max_blocks < 1 || num_blocks < 1)
+    return ATTN_VARLEN_ERR_INVALID_ARG;
+  // a page's 16-byte pieces and a token's elements are counted in 32 bits
+  if ((int64_t)num_kv_heads * head_size > (1 << 22)) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (!k_cache || !v_cache) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u)
+    return ATTN_VARLEN_ERR_MISALIGNED;
+  return ATTN_VARLEN_OK;
+}
+
+// Non-null, 4-byte aligned int32 arrays.
+int check_arrays(std::initializer_list<const void*> ptrs) {
+  uintptr_t mis = 0;
+  for (const void* p : ptrs) {
+    if (!p) return ATTN_VARLEN_ERR_INVALID_ARG;
+    mis |= reinterpret_cast<uintptr_t>(p);
+  }
+  return mis & 3u ? ATTN_VARLEN_ERR_MISALIGNED : ATTN_VARLEN_OK;
+}
+
+// The device's part of a CacheShape.
+int cache_shape(avp::CacheShape& c, void* k_cache, void* v_cache, int num_seqs, int num_kv_heads,
+                int head_size, int max_blocks, int num_blocks) {
+  int dev = 0;
+  int rc = current_device(&dev);
+  if (rc) return rc;
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState& st = g_dev[dev];
+  if ((rc = probe_device(dev, st))) return rc;
+  if (!g_page_status_ptr[dev]) {
+    void* ptr = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&ptr, g_page_status);
+    if (e != cudaSuccess) return fail_cuda(e);
+    if (!ptr) return ATTN_VARLEN_ERR_CUDA;
+    g_page_status_ptr[dev] = static_cast<int*>(ptr);
+  }
+  c = {k_cache, v_cache, g_page_status_ptr[dev], num_seqs, num_kv_heads, head_size,
+       max_blocks, num_blocks, st.sm_count};
+  return ATTN_VARLEN_OK;
+}
+
+// Read and clear the paged-cache operators' status word (null: they never ran
+// on the device).  The stream has been synchronised.
+int read_and_clear_page_status(int* word) {
+  if (!word) return ATTN_VARLEN_OK;
+  int status = 0;
+  cudaError_t e = cudaMemcpy(&status, word, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return fail_cuda(e);
+  if (status == 0) return ATTN_VARLEN_OK;
+  const int zero = 0;
+  e = cudaMemcpy(word, &zero, sizeof(int), cudaMemcpyHostToDevice);
+  if (e != cudaSuccess) return fail_cuda(e);
+  if (status & avp::kPageStatusTimeout) return ATTN_VARLEN_ERR_DEVICE_TIMEOUT;
+  if (status & avp::kPageStatusBadBlock) return ATTN_VARLEN_ERR_BAD_BLOCK_TABLE;
+  if (status & avp::kPageStatusNoBlock) return ATTN_VARLEN_ERR_NO_FREE_BLOCK;
+  if (status & avp::kPageStatusBadDraft) return ATTN_VARLEN_ERR_BAD_DRAFT;
+  return ATTN_VARLEN_ERR_BAD_ROW;
+}
+
 int read_and_clear_status(void* ws, cudaStream_t stream) {
   cudaError_t e = cudaStreamSynchronize(stream);
   int status = 0;
@@ -490,17 +562,176 @@ int chunk_delta_rule_output(const void* q, const void* k, const void* v, const v
   return map_cuda(avp::launch_chunk_o(p, g_encode, stream));
 }
 
+int paged_attn_cache_write(const void* key, const void* value, void* k_cache, void* v_cache,
+                           const int32_t* block_tables, const int32_t* seq_lens,
+                           const int32_t* cu_seqlens, int num_seqs, int total_tokens,
+                           int num_kv_heads, int head_size, int block_size,
+                           int max_blocks_per_seq, int num_blocks, int64_t key_token_stride,
+                           int64_t key_head_stride, int64_t value_token_stride,
+                           int64_t value_head_stride, cudaStream_t stream) {
+  if (num_seqs < 0 || total_tokens < 0) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_tokens == 0) return ATTN_VARLEN_OK;
+  int rc = check_cache(k_cache, v_cache, num_kv_heads, head_size, block_size, max_blocks_per_seq,
+                       num_blocks);
+  if (!rc) rc = check_arrays({block_tables, seq_lens, cu_seqlens});
+  if (rc) return rc;
+  if (!key || !value) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(key) | reinterpret_cast<uintptr_t>(value)) & 15u)
+    return ATTN_VARLEN_ERR_MISALIGNED;
+  for (int64_t s : {key_token_stride, key_head_stride, value_token_stride, value_head_stride}) {
+    if (s < 0 || s > (1ll << 40)) return ATTN_VARLEN_ERR_INVALID_ARG;
+    if (s & 7) return ATTN_VARLEN_ERR_MISALIGNED;
+  }
+  avp::CacheWriteParams p;
+  if ((rc = cache_shape(p.c, k_cache, v_cache, num_seqs, num_kv_heads, head_size,
+                        max_blocks_per_seq, num_blocks)))
+    return rc;
+  p.key = key;
+  p.value = value;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.cu = cu_seqlens;
+  p.total_tokens = total_tokens;
+  p.key_token = key_token_stride;
+  p.key_head = key_head_stride;
+  p.value_token = value_token_stride;
+  p.value_head = value_head_stride;
+  return map_cuda(avp::launch_cache_write(p, stream));
+}
+
+int paged_attn_cache_accept(void* k_cache, void* v_cache, const int32_t* block_tables,
+                            const int32_t* seq_lens, const int32_t* cu_seqlens,
+                            const int32_t* accepted, const int32_t* num_accepted, int num_seqs,
+                            int max_accepted, int num_kv_heads, int head_size, int block_size,
+                            int max_blocks_per_seq, int num_blocks, int32_t* new_lens,
+                            cudaStream_t stream) {
+  if (num_seqs < 0 || max_accepted < 1) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (num_seqs == 0) return ATTN_VARLEN_OK;
+  int rc = check_cache(k_cache, v_cache, num_kv_heads, head_size, block_size, max_blocks_per_seq,
+                       num_blocks);
+  if (!rc)
+    rc = check_arrays({block_tables, seq_lens, cu_seqlens, accepted, num_accepted, new_lens});
+  if (rc) return rc;
+  avp::CacheAcceptParams p;
+  if ((rc = cache_shape(p.c, k_cache, v_cache, num_seqs, num_kv_heads, head_size,
+                        max_blocks_per_seq, num_blocks)))
+    return rc;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.cu = cu_seqlens;
+  p.accepted = accepted;
+  p.num_accepted = num_accepted;
+  p.max_accepted = max_accepted;
+  p.new_lens = new_lens;
+  return map_cuda(avp::launch_cache_accept(p, stream));
+}
+
+int paged_attn_cache_free(const int32_t* block_tables, int32_t* seq_lens, int32_t* refs,
+                          const int32_t* rows, int num_rows, int num_seqs, int block_size,
+                          int max_blocks_per_seq, int num_blocks, cudaStream_t stream) {
+  if (num_rows < 0 || num_seqs < 0) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (num_rows == 0) return ATTN_VARLEN_OK;
+  if (num_seqs < 1 || block_size != avp::kPageTokens || max_blocks_per_seq < 1 || num_blocks < 1)
+    return ATTN_VARLEN_ERR_INVALID_ARG;
+  int rc = check_arrays({block_tables, seq_lens, refs, rows});
+  if (rc) return rc;
+  avp::CacheFreeParams p;
+  if ((rc = cache_shape(p.c, nullptr, nullptr, num_seqs, 0, 0, max_blocks_per_seq, num_blocks)))
+    return rc;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.refs = refs;
+  p.rows = rows;
+  p.num_rows = num_rows;
+  return map_cuda(avp::launch_cache_free(p, stream));
+}
+
+size_t paged_attn_cache_fork_workspace_size(int num_forks, int num_seqs) {
+  if (num_forks < 0 || num_seqs < 0) return 0;
+  return 4 * (2 * (size_t)num_seqs + 2 * (size_t)num_forks);
+}
+
+int paged_attn_cache_fork(void* k_cache, void* v_cache, int32_t* block_tables, int32_t* seq_lens,
+                          int32_t* refs, const int32_t* src, const int32_t* dst, int num_forks,
+                          int num_seqs, int num_kv_heads, int head_size, int block_size,
+                          int max_blocks_per_seq, int num_blocks, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+  if (num_forks < 0 || num_seqs < 0) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (num_forks == 0) return ATTN_VARLEN_OK;
+  if (num_seqs < 1) return ATTN_VARLEN_ERR_INVALID_ARG;
+  int rc = check_cache(k_cache, v_cache, num_kv_heads, head_size, block_size, max_blocks_per_seq,
+                       num_blocks);
+  if (!rc) rc = check_arrays({block_tables, seq_lens, refs, src, dst, workspace});
+  if (rc) return rc;
+  if (workspace_bytes < paged_attn_cache_fork_workspace_size(num_forks, num_seqs))
+    return ATTN_VARLEN_ERR_WORKSPACE_SMALL;
+  avp::CacheForkParams p;
+  if ((rc = cache_shape(p.c, k_cache, v_cache, num_seqs, num_kv_heads, head_size,
+                        max_blocks_per_seq, num_blocks)))
+    return rc;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.refs = refs;
+  p.src = src;
+  p.dst = dst;
+  p.num_forks = num_forks;
+  p.owner = static_cast<int32_t*>(workspace);
+  p.is_src = p.owner + num_seqs;
+  p.state = p.is_src + num_seqs;
+  p.pages = p.state + num_forks;
+  return map_cuda(avp::launch_cache_fork(p, stream));
+}
+
+size_t paged_attn_cache_compact_workspace_size(int num_blocks) {
+  if (num_blocks < 0) return 0;
+  return 4 * (1 + 3 * (size_t)num_blocks);
+}
+
+int paged_attn_cache_compact(void* k_cache, void* v_cache, const int32_t* block_tables,
+                             const int32_t* seq_lens, const int32_t* refs, int num_seqs,
+                             int num_kv_heads, int head_size, int block_size,
+                             int max_blocks_per_seq, int num_blocks, int32_t* block_tables_out,
+                             int32_t* refs_out, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
+  if (num_seqs < 0) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (num_seqs == 0) return ATTN_VARLEN_OK;
+  int rc = check_cache(k_cache, v_cache, num_kv_heads, head_size, block_size, max_blocks_per_seq,
+                       num_blocks);
+  if (!rc) rc = check_arrays({block_tables, seq_lens, refs, block_tables_out, refs_out, workspace});
+  if (rc) return rc;
+  if (workspace_bytes < paged_attn_cache_compact_workspace_size(num_blocks))
+    return ATTN_VARLEN_ERR_WORKSPACE_SMALL;
+  avp::CacheCompactParams p;
+  if ((rc = cache_shape(p.c, k_cache, v_cache, num_seqs, num_kv_heads, head_size,
+                        max_blocks_per_seq, num_blocks)))
+    return rc;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.refs = refs;
+  p.block_tables_out = block_tables_out;
+  p.refs_out = refs_out;
+  p.moves = static_cast<int32_t*>(workspace);
+  p.remap = p.moves + 1;
+  p.from = p.remap + num_blocks;
+  p.to = p.from + num_blocks;
+  return map_cuda(avp::launch_cache_compact(p, stream));
+}
+
 int attn_varlen_check(cudaStream_t stream) {
   int dev = 0;
   int rc = current_device(&dev);
   if (rc) return rc;
   void* ws = nullptr;
+  int* word = nullptr;
   {
     std::lock_guard<std::mutex> lock(g_mu);
     ws = g_dev[dev].ws;
+    word = g_page_status_ptr[dev];
   }
-  if (!ws) return map_cuda(cudaStreamSynchronize(stream));
-  return read_and_clear_status(ws, stream);
+  rc = ws ? read_and_clear_status(ws, stream) : map_cuda(cudaStreamSynchronize(stream));
+  if (rc == ATTN_VARLEN_ERR_CUDA) return rc;
+  const int page_rc = read_and_clear_page_status(word);
+  return rc ? rc : page_rc;
 }
 
 int attn_varlen_check_ws(void* workspace, cudaStream_t stream) {
@@ -543,7 +774,14 @@ const char* attn_varlen_strerror(int code) {
     case ATTN_VARLEN_ERR_WORKSPACE_SMALL: return "workspace smaller than attn_varlen_workspace_size()";
     case ATTN_VARLEN_ERR_DRIVER: return "cuTensorMapEncodeTiled unavailable or failed";
     case ATTN_VARLEN_ERR_BAD_BLOCK_TABLE:
-      return "paged decode: a block table entry was outside [0, num_blocks)";
+      return "paged cache: a block table entry was outside [0, num_blocks), or a position past the "
+             "table";
+    case ATTN_VARLEN_ERR_BAD_DRAFT:
+      return "paged cache: a draft's parent, an accepted index or a count of drafts was out of range";
+    case ATTN_VARLEN_ERR_NO_FREE_BLOCK: return "paged cache: a fork found no free page";
+    case ATTN_VARLEN_ERR_BAD_ROW:
+      return "paged cache: a row was out of range, named twice or not free, or a page was freed "
+             "that no row holds";
     case ATTN_VARLEN_ERR_NOALLOC_LIMIT:
       return "num_seqs exceeds ATTN_VARLEN_NOALLOC_MAX_SEQS (1024), the fixed scratch of "
              "attn_varlen_fwd_noalloc";

@@ -1,0 +1,567 @@
+// The operators that fill and manage the paged key/value cache: write, accept,
+// free, fork, compact (include/paged_attn_cache.h has what each computes).
+// They move 2-byte elements and count pages; no floating-point arithmetic.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "paged_cache_internal.h"
+#include "paged_walk.cuh"
+#include "ptx.cuh"
+
+namespace avp {
+namespace {
+
+constexpr int kPage = kPageTokens;
+
+// A sequence's new tokens: packed rows [lo, lo + n), the last n positions of
+// its len tokens.  A negative slice is empty, rows outside the packed tensor
+// are never read, a negative length is 0.
+struct NewTokens {
+  int lo, n, len;
+};
+
+__device__ __forceinline__ NewTokens new_tokens(const int32_t* __restrict__ cu,
+                                                const int32_t* __restrict__ seq_lens, int i,
+                                                int total) {
+  NewTokens t;
+  t.lo = max(__ldg(cu + i), 0);
+  t.n = max(min(__ldg(cu + i + 1), total) - t.lo, 0);
+  t.len = max(__ldg(seq_lens + i), 0);
+  return t;
+}
+
+// --------------------------------------------------------------------- write
+// Bound by HBM: every new element is read once and written once.  A unit is
+// one page of one sequence for a group of heads, so that the tokens of a page
+// meet in one CTA: the value cache is token-fastest, and a thread that holds
+// 8 tokens of 8 dimensions turns them over in registers and writes whole
+// 16-byte pieces of 8 tokens (32 bytes with its neighbour).  Keys keep their
+// 8-element pieces: 16 lanes write 16 tokens of a piece, 256 bytes in a row.
+constexpr int kWriteThreads = 256;
+
+struct WriteUnit {
+  int first, pages;  // pages [first, first + pages) of the sequence take new tokens
+};
+
+__device__ __forceinline__ WriteUnit write_pages(const NewTokens& t, int max_blocks) {
+  const long long cap = (long long)max_blocks * kPage;
+  const int begin = max(t.len - t.n, 0);
+  const int end = (int)min((long long)t.len, cap);
+  WriteUnit w;
+  w.first = begin / kPage;
+  w.pages = t.n > 0 && end > begin ? (end - 1) / kPage - w.first + 1 : 0;
+  return w;
+}
+
+__global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(
+    const __grid_constant__ CacheWriteParams p, int head_group) {
+  __shared__ UnitScratch scratch;
+  const int groups = (p.c.num_kv_heads + head_group - 1) / head_group;
+  auto count = [&](int i) -> long long {
+    return (long long)write_pages(new_tokens(p.cu, p.seq_lens, i, p.total_tokens), p.c.max_blocks)
+               .pages * groups;
+  };
+  const UnitRange r =
+      locate_units<kWriteThreads>(p.c.num_seqs, blockIdx.x, gridDim.x, scratch, count);
+  const int tid = threadIdx.x;
+  const int pieces = p.c.head_size / 8;  // 16-byte pieces of a head's elements
+  const uint16_t* key = static_cast<const uint16_t*>(p.key);
+  const uint16_t* value = static_cast<const uint16_t*>(p.value);
+  uint16_t* kc = static_cast<uint16_t*>(p.c.k_cache);
+  uint16_t* vc = static_cast<uint16_t*>(p.c.v_cache);
+  int seq = r.seq;
+  long long off = r.off;
+  for (long long u = r.u0; u < r.u1; ++u, ++off) {
+    NewTokens t;
+    WriteUnit w;
+    for (;; ++seq, off = 0) {
+      if (seq >= p.c.num_seqs) return;  // only if the lengths changed under the kernel
+      t = new_tokens(p.cu, p.seq_lens, seq, p.total_tokens);
+      w = write_pages(t, p.c.max_blocks);
+      if (off < (long long)w.pages * groups) break;
+    }
+    const int page = w.first + (int)(off / groups);
+    const int g0 = (int)(off % groups) * head_group;
+    const int heads = min(head_group, p.c.num_kv_heads - g0);
+    if (tid == 0 && t.len > p.c.max_blocks * (long long)kPage)
+      atomicOr(p.c.status, kPageStatusBadBlock);
+    const int id = __ldg(p.block_tables + (size_t)seq * p.c.max_blocks + page);
+    if (id < 0 || id >= p.c.num_blocks) {
+      if (tid == 0) atomicOr(p.c.status, kPageStatusBadBlock);
+      continue;
+    }
+    // slots [s0, s1) of the page take packed rows row0 + slot
+    const int base = t.len - t.n;
+    const int s0 = max(base - page * kPage, 0), s1 = min(t.len - page * kPage, kPage);
+    const long long row0 = (long long)t.lo + page * kPage - base;
+    const size_t head0 = (size_t)id * p.c.num_kv_heads + g0;
+    // keys: item = (head, piece, slot), slots fastest
+    const int kitems = heads * pieces * kPage;
+#pragma unroll 4
+    for (int x = tid; x < kitems; x += kWriteThreads) {
+      const int slot = x % kPage, piece = (x / kPage) % pieces, h = x / (kPage * pieces);
+      if (slot < s0 || slot >= s1) continue;
+      const uint4 e = *reinterpret_cast<const uint4*>(key + (row0 + slot) * p.key_token +
+                                                      (g0 + h) * p.key_head + piece * 8);
+      *reinterpret_cast<uint4*>(kc + ((head0 + h) * pieces + piece) * (kPage * 8) + slot * 8) = e;
+    }
+    // values: item = (head, 8 dimensions, 8 slots)
+    const int vitems = heads * pieces * 2;
+    for (int x = tid; x < vitems; x += kWriteThreads) {
+      const int half = x & 1, piece = (x >> 1) % pieces, h = x / (2 * pieces);
+      const int lo = max(s0 - half * 8, 0), hi = min(s1 - half * 8, 8);
+      if (lo >= hi) continue;
+      uint32_t e[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i >= lo && i < hi) {
+          const uint4 v = *reinterpret_cast<const uint4*>(
+              value + (row0 + half * 8 + i) * p.value_token + (g0 + h) * p.value_head + piece * 8);
+          e[i][0] = v.x, e[i][1] = v.y, e[i][2] = v.z, e[i][3] = v.w;
+        } else {
+          e[i][0] = e[i][1] = e[i][2] = e[i][3] = 0;
+        }
+      }
+      uint16_t* dst =
+          vc + ((head0 + h) * p.c.head_size + piece * 8) * kPage + half * 8;
+      if (hi - lo == 8) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          // tokens 2 j, 2 j + 1 of dimension d in one word
+          const uint32_t sel = d & 1 ? 0x7632u : 0x5410u;
+          uint4 o;
+          o.x = __byte_perm(e[0][d >> 1], e[1][d >> 1], sel);
+          o.y = __byte_perm(e[2][d >> 1], e[3][d >> 1], sel);
+          o.z = __byte_perm(e[4][d >> 1], e[5][d >> 1], sel);
+          o.w = __byte_perm(e[6][d >> 1], e[7][d >> 1], sel);
+          *reinterpret_cast<uint4*>(dst + d * kPage) = o;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i < lo || i >= hi) continue;
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+            dst[d * kPage + i] = (uint16_t)(e[i][d >> 1] >> (16 * (d & 1)));
+        }
+      }
+    }
+  }
+}
+
+// -------------------------------------------------------------------- accept
+// Draft a_m moves to slot m of the drafts, and a_m >= m with a increasing, so
+// a move never overwrites a draft that a later one reads.  Each thread owns
+// one element position (a value dimension, or an 8-element piece of a key) and
+// moves it for every accepted draft in order, eight loads ahead of their
+// stores: threads never touch one another's elements, so no barrier is needed
+// between moves.
+constexpr int kAcceptThreads = 128;
+constexpr int kAcceptBatch = 128;  // moves resolved through the table at a time
+
+__global__ void __launch_bounds__(kAcceptThreads) cache_accept_kernel(
+    const __grid_constant__ CacheAcceptParams p) {
+  __shared__ int s_from[kAcceptBatch], s_to[kAcceptBatch];            // page ids, -1: not moved
+  __shared__ uint8_t s_fslot[kAcceptBatch], s_tslot[kAcceptBatch];
+  __shared__ int s_stop;
+  const int seq = blockIdx.x, tid = threadIdx.x;
+  const NewTokens t = new_tokens(p.cu, p.seq_lens, seq, INT_MAX);
+  const int base = t.len - t.n;
+  const int asked = __ldg(p.num_accepted + seq);
+  int take = max(min(asked, min(p.max_accepted, t.n)), 0);
+  bool bad = take != asked;
+  const int32_t* list = p.accepted + (size_t)seq * p.max_accepted;
+  const int32_t* table = p.block_tables + (size_t)seq * p.c.max_blocks;
+  const int pieces = p.c.head_size / 8;
+  const int values = p.c.num_kv_heads * p.c.head_size, keys = p.c.num_kv_heads * pieces;
+  const int item = blockIdx.y * kAcceptThreads + tid;  // value elements, then key pieces
+  for (int m0 = 0; m0 < take; m0 += kAcceptBatch) {
+    if (tid == 0) s_stop = kAcceptBatch;
+    __syncthreads();
+    const int n = min(kAcceptBatch, take - m0);
+    if (tid < n) {
+      const int m = m0 + tid;
+      const int a = __ldg(list + m);
+      const int prev = m ? __ldg(list + m - 1) : -1;
+      // increasing entries from 0 on have a >= m
+      const bool holds = a > prev && a >= m && a < t.n;
+      if (!holds) atomicMin(&s_stop, tid);
+      const long long src = (long long)base + a, dst = (long long)base + m;
+      int from = -1, to = -1;
+      if (holds && a != m && dst >= 0) {  // dst < src
+        if (src < (long long)p.c.max_blocks * kPage) {
+          from = __ldg(table + src / kPage);
+          to = __ldg(table + dst / kPage);
+        }
+        if (from < 0 || from >= p.c.num_blocks || to < 0 || to >= p.c.num_blocks) {
+          atomicOr(p.c.status, kPageStatusBadBlock);
+          from = -1;
+        }
+      }
+      s_from[tid] = from;
+      s_to[tid] = to;
+      s_fslot[tid] = (uint8_t)(src & (kPage - 1));
+      s_tslot[tid] = (uint8_t)(dst & (kPage - 1));
+    }
+    __syncthreads();
+    const int stop = min(n, s_stop);
+    if (item < values) {
+      uint16_t* vc = static_cast<uint16_t*>(p.c.v_cache) + (size_t)item * kPage;
+      const size_t page = (size_t)values * kPage;
+      for (int m = 0; m < stop; m += 8) {
+        uint16_t e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (m + i < stop && s_from[m + i] >= 0) e[i] = vc[s_from[m + i] * page + s_fslot[m + i]];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (m + i < stop && s_from[m + i] >= 0) vc[s_to[m + i] * page + s_tslot[m + i]] = e[i];
+      }
+    } else if (item < values + keys) {
+      uint4* kc = static_cast<uint4*>(p.c.k_cache) + (size_t)(item - values) * kPage;
+      const size_t page = (size_t)keys * kPage;
+      for (int m = 0; m < stop; m += 8) {
+        uint4 e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (m + i < stop && s_from[m + i] >= 0) e[i] = kc[s_from[m + i] * page + s_fslot[m + i]];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (m + i < stop && s_from[m + i] >= 0) kc[s_to[m + i] * page + s_tslot[m + i]] = e[i];
+      }
+    }
+    __syncthreads();  // the batch's lists are read
+    if (stop < n) {   // out of order: acceptance ends here
+      take = m0 + stop;
+      bad = true;
+    }
+  }
+  if (blockIdx.y == 0 && tid == 0) {
+    p.new_lens[seq] = max(base + take, 0);
+    if (bad) atomicOr(p.c.status, kPageStatusBadDraft);
+  }
+}
+
+// ---------------------------------------------------------------------- free
+// One CTA per named row.  The exchange of the length with 0 makes one of
+// several frees of a row the one that counts; counts only go down by integer
+// atomics, so the result does not depend on their order.
+constexpr int kFreeThreads = 128;
+
+__global__ void __launch_bounds__(kFreeThreads) cache_free_kernel(
+    const __grid_constant__ CacheFreeParams p) {
+  __shared__ int s_len;
+  const int row = __ldg(p.rows + blockIdx.x);
+  if (row < 0 || row >= p.c.num_seqs) {
+    if (threadIdx.x == 0) atomicOr(p.c.status, kPageStatusBadRow);
+    return;
+  }
+  if (threadIdx.x == 0) s_len = atomicExch(p.seq_lens + row, 0);
+  __syncthreads();
+  const int len = s_len;
+  const int pages = len > 0 ? min((len - 1) / kPage + 1, p.c.max_blocks) : 0;
+  const int32_t* table = p.block_tables + (size_t)row * p.c.max_blocks;
+  for (int i = threadIdx.x; i < pages; i += kFreeThreads) {
+    const int id = __ldg(table + i);
+    if (id < 0 || id >= p.c.num_blocks) {
+      atomicOr(p.c.status, kPageStatusBadBlock);
+    } else if (atomicSub(p.refs + id, 1) <= 0) {
+      atomicAdd(p.refs + id, 1);
+      atomicOr(p.c.status, kPageStatusBadRow);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------- fork
+// A plan (one CTA) decides which forks hold, which of them need a page and
+// which page each gets; the forks themselves then run side by side.  The plan
+// reads counts and lengths before any fork changes them.
+constexpr int kPlanThreads = 1024;
+constexpr int kForkThreads = 256;
+constexpr int kForkParts = 4;  // CTAs per fork
+constexpr int kRefused = -2, kNoPage = -1;
+
+// Exclusive scan over the CTA's threads; `total` gets the sum.
+__device__ __forceinline__ int block_exclusive(int x, int& total, int* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += y;
+  }
+  __syncthreads();  // s_warp's last readers are done
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  int w = s_warp[lane];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, d);
+    if (lane >= d) w += y;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return inc - x + (warp ? before : 0);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(
+    const __grid_constant__ CacheForkParams p) {
+  __shared__ int s_warp[32];
+  const int tid = threadIdx.x;
+  for (int r = tid; r < p.c.num_seqs; r += kPlanThreads) {
+    p.owner[r] = INT_MAX;
+    p.is_src[r] = 0;
+  }
+  __syncthreads();
+  auto inside = [&](int r) { return r >= 0 && r < p.c.num_seqs; };
+  for (int j = tid; j < p.num_forks; j += kPlanThreads) {
+    const int s = __ldg(p.src + j), d = __ldg(p.dst + j);
+    if (inside(s) && inside(d)) {
+      p.is_src[s] = 1;
+      atomicMin(p.owner + d, j);
+    }
+  }
+  __syncthreads();
+  int need = 0;  // pages the forks so far take
+  for (int j0 = 0; j0 < p.num_forks; j0 += kPlanThreads) {
+    const int j = j0 + tid;
+    bool holds = false, part = false;
+    if (j < p.num_forks) {
+      const int s = __ldg(p.src + j), d = __ldg(p.dst + j);
+      holds = inside(s) && inside(d) && __ldcg(p.owner + d) == j && !p.is_src[d] &&
+              p.seq_lens[d] <= 0;
+      if (!holds) atomicOr(p.c.status, kPageStatusBadRow);
+      // a row longer than its table has no page past the table to copy
+      part = holds && p.seq_lens[s] > 0 && p.seq_lens[s] % kPage != 0 &&
+             p.seq_lens[s] < p.c.max_blocks * (long long)kPage;
+    }
+    int total;
+    const int rank = need + block_exclusive(part ? 1 : 0, total, s_warp);
+    if (j < p.num_forks) p.state[j] = !holds ? kRefused : (part ? rank : kNoPage);
+    need += total;
+  }
+  // the `need` lowest free pages
+  int found = 0;
+  for (long long b0 = 0; b0 < p.c.num_blocks && found < need; b0 += 4 * kPlanThreads) {
+    const long long b = b0 + 4 * tid;
+    int free_mask = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (b + i < p.c.num_blocks && __ldcg(p.refs + b + i) <= 0) free_mask |= 1 << i;
+    int total;
+    int at = found + block_exclusive(__popc(free_mask), total, s_warp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (free_mask >> i & 1) {
+        if (at < need) p.pages[at] = (int)b + i;
+        ++at;
+      }
+    found += total;
+  }
+  __syncthreads();
+  for (int j = tid; j < p.num_forks; j += kPlanThreads) {
+    const int rank = p.state[j];
+    if (rank < 0) continue;
+    if (rank < found) {
+      p.state[j] = p.pages[rank];
+    } else {
+      p.state[j] = kRefused;
+      atomicOr(p.c.status, kPageStatusNoBlock);
+    }
+  }
+}
+
+// Copies 16-byte pieces [a, b) of one page to another, four in flight a thread.
+template <int THREADS>
+__device__ __forceinline__ void copy_pieces(const uint4* __restrict__ src, uint4* __restrict__ dst,
+                                            int a, int b) {
+  int i = a + (int)threadIdx.x;
+  for (; i + 3 * THREADS < b; i += 4 * THREADS) {
+    uint4 e[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) e[x] = __ldcs(src + i + x * THREADS);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) dst[i + x * THREADS] = e[x];
+  }
+  for (; i < b; i += THREADS) dst[i] = __ldcs(src + i);
+}
+
+__global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(
+    const __grid_constant__ CacheForkParams p) {
+  const int j = blockIdx.x, part = blockIdx.y;
+  const int fresh = p.state[j];
+  if (fresh == kRefused) return;
+  const int s = __ldg(p.src + j), d = __ldg(p.dst + j);
+  const int len = max(p.seq_lens[s], 0);
+  const int32_t* from = p.block_tables + (size_t)s * p.c.max_blocks;
+  int32_t* to = p.block_tables + (size_t)d * p.c.max_blocks;
+  const int full = min(len / kPage, p.c.max_blocks);
+  for (int i = part * kForkThreads + threadIdx.x; i < full; i += kForkParts * kForkThreads) {
+    const int id = from[i];
+    to[i] = id;
+    if (id < 0 || id >= p.c.num_blocks)
+      atomicOr(p.c.status, kPageStatusBadBlock);
+    else
+      atomicAdd(p.refs + id, 1);
+  }
+  if (part == 0 && threadIdx.x == 0) {
+    p.seq_lens[d] = len;
+    if (fresh >= 0) {
+      to[full] = fresh;
+      p.refs[fresh] = 1;
+    }
+  }
+  if (fresh < 0) return;
+  const int last = from[full];
+  if (last < 0 || last >= p.c.num_blocks) {
+    if (threadIdx.x == 0) atomicOr(p.c.status, kPageStatusBadBlock);
+    return;
+  }
+  const int page = p.c.num_kv_heads * p.c.head_size * 2;  // 16-byte pieces
+  const int a = (int)((long long)page * part / kForkParts);
+  const int b = (int)((long long)page * (part + 1) / kForkParts);
+  const uint4* k = static_cast<const uint4*>(p.c.k_cache);
+  const uint4* v = static_cast<const uint4*>(p.c.v_cache);
+  copy_pieces<kForkThreads>(k + (size_t)last * page,
+                            static_cast<uint4*>(p.c.k_cache) + (size_t)fresh * page, a, b);
+  copy_pieces<kForkThreads>(v + (size_t)last * page,
+                            static_cast<uint4*>(p.c.v_cache) + (size_t)fresh * page, a, b);
+}
+
+// ------------------------------------------------------------------- compact
+// A plan (one CTA) counts the used pages, U, and lists the moves: the i-th
+// lowest hole below U receives the i-th highest used page.  Both indexes
+// follow from one scan u(p) = used pages below p: a hole p is number p - u(p),
+// a used page p >= U is number U - u(p) - 1.  Then pages are copied and table
+// entries renamed side by side.
+constexpr int kCompactThreads = 256;
+constexpr int kPieceGroup = 1024;  // 16-byte pieces of a page one CTA copies at a time
+
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(
+    const __grid_constant__ CacheCompactParams p) {
+  __shared__ int s_warp[32];
+  const int tid = threadIdx.x, blocks = p.c.num_blocks;
+  int mine = 0;
+  for (long long b = tid; b < blocks; b += kPlanThreads) mine += p.refs[b] > 0;
+  int used;
+  block_exclusive(mine, used, s_warp);
+  int before = 0;  // used pages below b0
+  for (long long b0 = 0; b0 < blocks; b0 += 4 * kPlanThreads) {
+    const long long b = b0 + 4 * tid;
+    int ref[4], n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ref[i] = b + i < blocks ? p.refs[b + i] : 0;
+      n += ref[i] > 0;
+    }
+    int total;
+    int u = before + block_exclusive(n, total, s_warp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (b + i >= blocks) break;
+      const int id = (int)b + i;
+      if (ref[i] <= 0 && id < used) p.to[id - u] = id;
+      if (ref[i] > 0 && id >= used) p.from[used - u - 1] = id;
+      p.remap[id] = id;
+      p.refs_out[id] = ref[i];
+      u += ref[i] > 0;
+    }
+    // the holes below `used` are those before it less the used pages before it
+    if (b0 <= used && used < b0 + 4 * kPlanThreads) {
+      const int t = (int)((used - b0) / 4);
+      if (tid == t) {
+        int below = u;  // used pages below b + 4; take back those at or past `used`
+#pragma unroll
+        for (int i = 0; i < 4; ++i) below -= b + i >= used && ref[i] > 0;
+        *p.moves = used - below;
+      }
+    }
+    before += total;
+  }
+  if (used == blocks && tid == 0) *p.moves = 0;
+  __syncthreads();
+  const int moves = __ldcg(p.moves);
+  for (int i = tid; i < moves; i += kPlanThreads) {
+    const int a = __ldcg(p.from + i), b = __ldcg(p.to + i);
+    p.remap[a] = b;
+    p.refs_out[b] = __ldcg(p.refs + a);
+    p.refs_out[a] = 0;
+  }
+}
+
+__global__ void __launch_bounds__(kCompactThreads) compact_apply_kernel(
+    const __grid_constant__ CacheCompactParams p) {
+  const int moves = __ldg(p.moves);
+  const int page = p.c.num_kv_heads * p.c.head_size * 2;  // 16-byte pieces
+  const int groups = (page + kPieceGroup - 1) / kPieceGroup;
+  const long long tasks = (long long)moves * groups * 2;
+  for (long long x = blockIdx.x; x < tasks; x += gridDim.x) {
+    const bool value = x & 1;
+    const int g = (int)((x >> 1) % groups), i = (int)((x >> 1) / groups);
+    const size_t from = (size_t)__ldg(p.from + i) * page, to = (size_t)__ldg(p.to + i) * page;
+    uint4* c = static_cast<uint4*>(value ? p.c.v_cache : p.c.k_cache);
+    copy_pieces<kCompactThreads>(c + from, c + to, g * kPieceGroup,
+                                 min(page, (g + 1) * kPieceGroup));
+  }
+  const long long entries = (long long)p.c.num_seqs * p.c.max_blocks;
+  for (long long e = (long long)blockIdx.x * kCompactThreads + threadIdx.x; e < entries;
+       e += (long long)gridDim.x * kCompactThreads) {
+    const int row = (int)(e / p.c.max_blocks), col = (int)(e - (long long)row * p.c.max_blocks);
+    int id = p.block_tables[e];
+    if ((long long)col * kPage < __ldg(p.seq_lens + row)) {
+      if (id < 0 || id >= p.c.num_blocks)
+        atomicOr(p.c.status, kPageStatusBadBlock);
+      else
+        id = __ldg(p.remap + id);
+    }
+    p.block_tables_out[e] = id;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheWriteParams& p, cudaStream_t stream) {
+  // a page's heads in groups that give each thread one value item
+  const int pieces = p.c.head_size / 8;
+  const int group = std::min(p.c.num_kv_heads, std::max(1, kWriteThreads / (2 * pieces)));
+  const long long groups = (p.c.num_kv_heads + group - 1) / group;
+  // n tokens touch at most n / 16 + 2 pages
+  const long long most = ((long long)p.total_tokens / kPage + 2LL * p.c.num_seqs) * groups;
+  const int grid = (int)std::min<long long>(most, (long long)p.c.sm_count * 8);
+  cache_write_kernel<<<grid, kWriteThreads, 0, stream>>>(p, group);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_accept(const CacheAcceptParams& p, cudaStream_t stream) {
+  const long long items = (long long)p.c.num_kv_heads * p.c.head_size * 9 / 8;
+  const long long y = (items + kAcceptThreads - 1) / kAcceptThreads;
+  if (y > 65535) return cudaErrorInvalidConfiguration;
+  cache_accept_kernel<<<dim3(p.c.num_seqs, (unsigned)y), kAcceptThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_free(const CacheFreeParams& p, cudaStream_t stream) {
+  cache_free_kernel<<<p.num_rows, kFreeThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_fork(const CacheForkParams& p, cudaStream_t stream) {
+  fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  fork_apply_kernel<<<dim3(p.num_forks, kForkParts), kForkThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_compact(const CacheCompactParams& p, cudaStream_t stream) {
+  compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  compact_apply_kernel<<<p.c.sm_count * 4, kCompactThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace avp

@@ -1,0 +1,85 @@
+// Work that the host cannot count: every sequence has a number of units that
+// follows from its lengths on the device.  The units of all sequences, laid
+// end to end, are cut into one equal range per CTA.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace avp {
+namespace {
+
+// A CTA's range: units [u0, u1) of `total`; unit u0 is unit `off` of sequence
+// `seq`.  Empty when u0 == u1.
+struct UnitRange {
+  long long u0, u1, total;
+  long long off;
+  int seq;
+};
+
+struct UnitScratch {
+  long long warp_sum[32];
+  long long off;
+  int seq;
+};
+
+__device__ __forceinline__ long long warp_inclusive(long long x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// Range `part` of `parts`; every thread of the CTA takes part.  count(i) is
+// the units of sequence i.  Thread t sums a run of consecutive sequences, a
+// scan over the threads gives the total, and the thread whose run holds unit
+// u0 walks it.
+template <int THREADS, class Count>
+__device__ __forceinline__ UnitRange locate_units(int n, int part, int parts, UnitScratch& s,
+                                                  Count count) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int run = (n + THREADS - 1) / THREADS;
+  const int a = min(n, tid * run), b = min(n, a + run);
+  long long sum = 0;
+  for (int i = a; i < b; ++i) sum += count(i);
+  const long long inc = warp_inclusive(sum, lane);
+  if (lane == 31) s.warp_sum[warp] = inc;
+  if (tid == 0) {
+    s.seq = n;
+    s.off = 0;
+  }
+  __syncthreads();
+  long long before = inc - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += s.warp_sum[w];
+    total += s.warp_sum[w];
+  }
+  const int used = (int)(total < parts ? total : parts);  // ranges that hold a unit
+  UnitRange r;
+  r.total = total;
+  r.u0 = part < used ? total * part / used : total;
+  r.u1 = part < used ? total * (part + 1) / used : total;
+  if (r.u0 < r.u1 && before <= r.u0 && r.u0 < before + sum) {
+    long long at = before;
+    for (int i = a; i < b; ++i) {
+      const long long c = count(i);
+      if (r.u0 < at + c) {
+        s.seq = i;
+        s.off = r.u0 - at;
+        break;
+      }
+      at += c;
+    }
+  }
+  __syncthreads();
+  r.seq = s.seq;
+  r.off = s.off;
+  return r;
+}
+
+}  // namespace
+}  // namespace avp
