@@ -47,6 +47,8 @@ SYMBOLS = {
     "paged_attn_decode": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
     "chunk_delta_rule_output": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
                                      ctypes.c_float, _P, _P]),
+    "paged_attn_tree_workspace_size": (_SZ, [_I]),
+    "paged_attn_tree": (_I, [_P] * 7 + [_I] * 8 + [ctypes.c_float, _I, _P, _P, _SZ, _P]),
     "paged_attn_cache_write": (_I, [_P] * 7 + [_I] * 7 + [_L] * 4 + [_P]),
     "paged_attn_cache_accept": (_I, [_P] * 7 + [_I] * 7 + [_P, _P]),
     "paged_attn_cache_free": (_I, [_P] * 4 + [_I] * 5 + [_P]),
@@ -278,7 +280,7 @@ def chunk_delta_rule_output(q, k, v, h, g, chunk_size=64, scale=None, out=None, 
     return out
 
 
-# ------------------------------------------------------------- paged cache
+# ------------------------------------------- paged cache and drafted tokens
 # The operators below share their checks: every array on the first tensor's
 # device, int32 arrays contiguous, the two caches of one shape family.
 def _int32(device, **arrays):
@@ -468,3 +470,48 @@ def paged_attn_cache_compact(k_cache, v_cache, block_tables, seq_lens, refs, out
             refs.data_ptr(), s, hkv, d, bs, w, nb, tables_out.data_ptr(), refs_out.data_ptr(),
             ws.data_ptr(), size, h), "paged_attn_cache_compact")
     return tables_out, refs_out
+
+
+def paged_attn_tree(query, k_cache, v_cache, block_tables, seq_lens, cu_seqlens, parents=None,
+                    scale=None, out=None, stream=None):
+    """Attention of drafted tokens over a paged cache (include/paged_attn_tree.h).
+
+    query [total, Hq, D] of the caches' type, packed by cu_seqlens int32
+    [S + 1]: the last n tokens of row i, whose keys and values the cache holds
+    already (seq_lens counts them).  parents int32 [total]: the draft each
+    draft hangs on, an index within its row's drafts below its own, -1 for the
+    context; None for chains.  A draft sees the context, its ancestors and
+    itself.  scale: default D^-1/2.  Returns ``out`` (allocated like ``query``
+    when not given; rows that no sequence covers are left untouched).
+    """
+    import torch
+    nb, hkv, d, bs = _cache(k_cache, v_cache)
+    dev = k_cache.device
+    if block_tables.dim() != 2 or query.dim() != 3:
+        raise ValueError("query must be [total, Hq, D], block_tables [S, max_blocks]")
+    s, w = block_tables.shape
+    total, hq = query.shape[0], query.shape[1]
+    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)),
+           cu_seqlens=(cu_seqlens, (s + 1,)))
+    if parents is not None:
+        _int32(dev, parents=(parents, (total,)))
+    if scale is not None and not 0.0 < scale < float("inf"):
+        raise ValueError("scale must be positive and finite")
+    lib = load()
+    size = lib.paged_attn_tree_workspace_size(d)
+    with _On(dev, stream) as h:
+        if out is None:
+            out = torch.empty_like(query)
+        for name, t in (("query", query), ("out", out)):
+            if t.dtype != k_cache.dtype or not t.is_contiguous() or t.device != dev \
+                    or tuple(t.shape) != (total, hq, d):
+                raise ValueError(f"{name} must be a contiguous {k_cache.dtype} tensor "
+                                 f"{[total, hq, d]} on {dev}")
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        _done(lib.paged_attn_tree(
+            query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            seq_lens.data_ptr(), cu_seqlens.data_ptr(),
+            parents.data_ptr() if parents is not None else None, s, total, hq, hkv, d, bs, w, nb,
+            float(scale or 0.0), 1 if query.dtype == torch.float16 else 0, out.data_ptr(),
+            ws.data_ptr(), size, h), "paged_attn_tree")
+    return out

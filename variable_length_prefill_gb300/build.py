@@ -27,7 +27,8 @@ VARIANTS = {
                  ["-DATTN_VARLEN_WAIT_LIMIT_NS=50000000ull", "-DATTN_VARLEN_TEST_HOOKS=1"]),
 }
 SOURCES = ["attn_varlen_api.cu", "attn_varlen_kernels.cu", "attn_varlen_d256.cu",
-           "paged_decode.cu", "chunk_o.cu", "paged_cache.cu"]
+           "paged_decode.cu", "chunk_o.cu", "paged_cache.cu",
+           "paged_tree.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "-I", INCLUDE, "-I", CSRC]

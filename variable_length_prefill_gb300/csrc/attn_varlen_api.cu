@@ -18,8 +18,10 @@
 #include "chunk_o_internal.h"
 #include "paged_attn_cache.h"
 #include "paged_attn_decode.h"
+#include "paged_attn_tree.h"
 #include "paged_cache_internal.h"
 #include "paged_decode_internal.h"
+#include "paged_tree_internal.h"
 
 namespace {
 
@@ -715,6 +717,56 @@ int paged_attn_cache_compact(void* k_cache, void* v_cache, const int32_t* block_
   p.from = p.remap + num_blocks;
   p.to = p.from + num_blocks;
   return map_cuda(avp::launch_cache_compact(p, stream));
+}
+
+size_t paged_attn_tree_workspace_size(int head_size) {
+  return avp::paged_head_size_supported(head_size) ? avp::tree_workspace_bytes(head_size) : 0;
+}
+
+int paged_attn_tree(const void* query, const void* k_cache, const void* v_cache,
+                    const int32_t* block_tables, const int32_t* seq_lens,
+                    const int32_t* cu_seqlens, const int32_t* parents, int num_seqs, int total_q,
+                    int num_query_heads, int num_kv_heads, int head_size, int block_size,
+                    int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out,
+                    void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  static_assert(PAGED_ATTN_MAX_DRAFTS == avp::kTreeMaxDrafts, "drafts");
+  if (num_seqs < 0 || total_q < 0 || num_kv_heads < 1 || num_query_heads < 1 ||
+      num_query_heads % num_kv_heads != 0)
+    return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (dtype != PAGED_ATTN_BF16 && dtype != PAGED_ATTN_FP16) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_q == 0) return ATTN_VARLEN_OK;
+  int rc = check_cache(k_cache, v_cache, num_kv_heads, head_size, block_size, max_blocks_per_seq,
+                       num_blocks);
+  if (!rc) rc = check_arrays({block_tables, seq_lens, cu_seqlens, query, out, workspace});
+  if (rc) return rc;
+  if ((int64_t)num_query_heads * head_size > (1 << 22)) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(query) | reinterpret_cast<uintptr_t>(out) |
+       reinterpret_cast<uintptr_t>(workspace)) & 15u)
+    return ATTN_VARLEN_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(parents) & 3u) return ATTN_VARLEN_ERR_MISALIGNED;
+  if (!(scale == scale) || scale > 3.4e38f) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (workspace_bytes < paged_attn_tree_workspace_size(head_size))
+    return ATTN_VARLEN_ERR_WORKSPACE_SMALL;
+  avp::TreeParams p;
+  if ((rc = cache_shape(p.c, const_cast<void*>(k_cache), const_cast<void*>(v_cache), num_seqs,
+                        num_kv_heads, head_size, max_blocks_per_seq, num_blocks)))
+    return rc;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if ((rc = get_encoder())) return rc;
+  }
+  p.query = query;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.cu = cu_seqlens;
+  p.parents = parents;
+  p.out = out;
+  p.workspace = static_cast<uint8_t*>(workspace);
+  p.total_q = total_q;
+  p.num_query_heads = num_query_heads;
+  const double s = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)head_size);
+  p.scale_log2 = (float)(1.4426950408889634 * s);
+  return map_cuda(avp::launch_tree(p, dtype == PAGED_ATTN_FP16, g_encode, stream));
 }
 
 int attn_varlen_check(cudaStream_t stream) {
