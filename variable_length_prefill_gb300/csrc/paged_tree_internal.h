@@ -14,6 +14,8 @@
 namespace avp {
 
 constexpr int kTreeMaxDrafts = 256;
+constexpr int kTreeRows = 128;   // query rows of a tile (drafts x query heads of one KV head)
+constexpr int kTreeMaxCtas = 160;  // CTAs of the attention kernel at most (one per SM)
 
 struct TreeParams {
   CacheShape c;  // caches, status, sizes
@@ -29,7 +31,24 @@ struct TreeParams {
   float scale_log2;  // scale * log2(e)
 };
 
-size_t tree_workspace_bytes(int head_size);
+// Workspace: kTreeMaxCtas TreeOpen records, then fp32 partial results
+// [2 kTreeMaxCtas][head_size + 2][kTreeRows]: O, then the maximum and the sum.
+struct TreeOpen {
+  int valid;  // a row tile that this CTA begins and leaves to others to finish
+  int lo;     // first packed row of its sequence
+  int n;      // drafts
+  int g;      // KV head
+  int mt;     // row tile
+  int last;   // the CTA that finishes it
+  int pad[2];
+};
+
+__host__ __device__ constexpr size_t tree_parts_offset() { return sizeof(TreeOpen) * kTreeMaxCtas; }
+__host__ __device__ constexpr size_t tree_part_floats(int head_size) { return (size_t)(head_size + 2) * kTreeRows; }
+__host__ __device__ constexpr size_t tree_workspace_bytes(int head_size) {
+  return tree_parts_offset() + 2 * kTreeMaxCtas * tree_part_floats(head_size) * sizeof(float);
+}
+
 cudaError_t launch_tree(const TreeParams& p, bool fp16, EncodeTiledFn enc, cudaStream_t stream);
 
 }  // namespace avp
