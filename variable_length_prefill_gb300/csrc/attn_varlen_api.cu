@@ -751,10 +751,6 @@ int paged_attn_tree(const void* query, const void* k_cache, const void* v_cache,
   if ((rc = cache_shape(p.c, const_cast<void*>(k_cache), const_cast<void*>(v_cache), num_seqs,
                         num_kv_heads, head_size, max_blocks_per_seq, num_blocks)))
     return rc;
-  {
-    std::lock_guard<std::mutex> lock(g_mu);
-    if ((rc = get_encoder())) return rc;
-  }
   p.query = query;
   p.block_tables = block_tables;
   p.seq_lens = seq_lens;
@@ -766,7 +762,7 @@ int paged_attn_tree(const void* query, const void* k_cache, const void* v_cache,
   p.num_query_heads = num_query_heads;
   const double s = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)head_size);
   p.scale_log2 = (float)(1.4426950408889634 * s);
-  return map_cuda(avp::launch_tree(p, dtype == PAGED_ATTN_FP16, g_encode, stream));
+  return map_cuda(avp::launch_tree(p, dtype == PAGED_ATTN_FP16, stream));
 }
 
 int attn_varlen_check(cudaStream_t stream) {

@@ -15,14 +15,17 @@
 //           pages of a tile one page apart, so S = Q K^T runs as two products:
 //           the first halves of all pages of the tile, then the second halves
 //           (a fixed permutation of the tile's tokens).
-//   values  a page is [D][16 tokens], 32 bytes a row: one tiled copy with the
-//           32-byte swizzle makes it the K-major operand of one 16-token step
-//           of O += P V.
+//   values  a page is [D][16 tokens], 32 bytes a row: the K-major operand of one
+//           16-token step of O += P V in the 32-byte swizzle, but for the
+//           swizzle itself, which exchanges the two halves of the rows d with
+//           bit 2 set.  One bulk copy per page, and two warps exchange those
+//           halves in shared memory.  (A tiled copy can do the swizzle, in
+//           32-byte rows; it held the 64 x 4096 case to 322 us.)
 // P is rounded to the cache type and written to TMEM over its scores, in token
 // order, for the value product.
 //
 // A persistent CTA per SM (NG softmax groups of four warps, a producer, an MMA
-// issuer) takes an equal share of all (sequence, KV head, row tile, key tile)
+// issuer, two warps that ready the values) takes an equal share of all (sequence, KV head, row tile, key tile)
 // units in that order (paged_walk.cuh), so a long sequence is split over many
 // CTAs without the host knowing a length.  Row tiles that begin and end in one
 // CTA are written to `out`; the others leave unnormalised partial results in
@@ -35,11 +38,10 @@
 // at the end of the row tile.  For D = 256 one group works on both score
 // buffers (two 256-column accumulators do not fit).
 //
-// A weight of 0 does not silence a NaN or an infinity in the values, so before
-// the value product of a tile that holds drafts or slots past the last token,
-// the group that owns it clears those slots, and the non-finite values of
-// drafts, in shared memory; the latter are added at the end to the rows that
-// see them.
+// A weight of 0 does not silence a NaN or an infinity in the values, so in a
+// tile that holds drafts or slots past the last token, the warps that ready the
+// values clear those slots, and the non-finite values of drafts; the latter are
+// added at the end to the rows that see them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -59,6 +61,7 @@ constexpr int kMaxDevices = 64;
 constexpr int kAncWords = kTreeMaxDrafts / 32;
 constexpr int kAncStride = kAncWords + 1;  // words between rows of the ancestor table
 constexpr int kMaskDepth = 8;              // key tiles whose page masks are kept
+constexpr int kFlagDepth = 8;              // segments whose flags are kept
 
 template <int D>
 struct TreeCfg {
@@ -69,8 +72,10 @@ struct TreeCfg {
   static constexpr uint32_t UNIT = BLK * PAGE;           // a key or value tile
   static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? 5 : 4);
   static constexpr int SOFTMAX = 128 * NG;  // softmax threads
-  static constexpr int THREADS = SOFTMAX + 64;
-  static constexpr int PROD = 4 * NG, MMA = 4 * NG + 1;  // warps
+  static constexpr int THREADS = SOFTMAX + 128;
+  // Warps past the softmax groups.  The MMA issuer comes last: it then shares
+  // its scheduler with the groups' last warps, which have no rows below 97.
+  static constexpr int FIX = 4 * NG, PROD = 4 * NG + 2, MMA = 4 * NG + 3;
   // the page masks of tile t are overwritten by tile t + kMaskDepth, whose
   // keys cannot be loaded before t's values are released
   static_assert(2 * kMaskDepth - 3 >= STAGES, "mask depth");
@@ -88,28 +93,17 @@ struct TreeCfg {
   static constexpr uint32_t BAR = (MASK + kMaskDepth * 4 + 7) & ~7u;
   // barriers
   static constexpr int FULL = 0, EMPTY = STAGES, S_FULL = 2 * STAGES, P_READY = S_FULL + 2,
-                       PV_DONE = P_READY + 2, Q_READY = PV_DONE + 2, DRAIN = Q_READY + 1,
-                       NBAR = DRAIN + 1;
+                       PV_DONE = P_READY + 2, Q_READY = PV_DONE + 2, V_READY = Q_READY + 1,
+                       DRAIN = V_READY + STAGES, NBAR = DRAIN + 1;
   static constexpr uint32_t TMEM_SLOT = BAR + NBAR * 8;
   static constexpr uint32_t ABORT = TMEM_SLOT + 4;
-  static constexpr uint32_t NONFINITE = ABORT + 4;
-  static constexpr uint32_t BYTES = NONFINITE + 4 + 1024;  // + alignment slack
+  static constexpr uint32_t ODD = ABORT + 4;  // [kFlagDepth][2]
+  static constexpr uint32_t BYTES = ODD + kFlagDepth * 8 + 1024;  // + alignment slack
+  // a segment has at least two units, so the warps that ready values are at
+  // most STAGES / 2 segments ahead of the softmax groups
+  static_assert(kFlagDepth > STAGES / 2, "flag depth");
   static_assert(BYTES + 512 <= 232448, "one CTA per SM");
 };
-
-struct TreeKernelParams {
-  CUtensorMap vmap;  // values as {16, D, Hkv, num_blocks}, box {16, D, 1, 1}, 32-byte swizzle
-  TreeParams t;
-};
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int c0,
-                                            int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-      : "memory");
-}
 
 // The two 16-bit types: packing, the exponent that marks a NaN or an infinity,
 // and the operand format of the instruction descriptor.
@@ -203,12 +197,18 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
+// Barrier among the softmax warps.  Like the tcgen05 loads and stores it wants
+// the whole warp at once, which lane-dependent branches before it do not promise.
+__device__ __forceinline__ void softmax_barrier(int threads) {
+  __syncwarp();
+  named_bar_sync(1, threads);
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
-    tree_kernel(const __grid_constant__ TreeKernelParams kp) {
+    tree_kernel(const __grid_constant__ TreeParams p) {
   using C = TreeCfg<D>;
   constexpr int NT = C::NT, NG = C::NG, BLK = C::BLK;
-  const TreeParams& p = kp.t;
   extern __shared__ uint8_t smem_raw[];
   __shared__ UnitScratch scratch;
   const uint32_t raw = smem_u32(smem_raw);
@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bar(C::FULL + s), 1);
       mbar_init(bar(C::EMPTY + s), 1);
+      mbar_init(bar(C::V_READY + s), 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(C::S_FULL + b), 1);
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  __syncwarp();
   if (warp == 0) {
     tmem_alloc(base + C::TMEM_SLOT, 512);
     tmem_relinquish();
@@ -265,7 +267,6 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     // Page ids come 32 at a time, one read ahead of their use; lane b of the
     // warp copies page b of a tile.
     constexpr int TPC = 32 / BLK;  // key tiles per read of ids
-    if (lane == 0) tmap_prefetch(&kp.vmap);
     uint32_t issued = 0;
     bool ok = true;
     while (ok && walk.next(p, group, x)) {
@@ -290,16 +291,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           mbar_arrive_expect_tx(full, __popc(mask) * C::PAGE);
         }
         __syncwarp();
-        if (there) {
-          const uint32_t dst = slot(u) + lane * C::PAGE;
-          if (value)
-            tma_load_4d(dst, &kp.vmap, full, 0, 0, x.g, page);
-          else
-            bulk_copy_g2s(dst,
-                          static_cast<const T*>(p.c.k_cache) +
-                              ((size_t)page * p.c.num_kv_heads + x.g) * (D * kPageTokens),
-                          C::PAGE, full);
-        }
+        if (there)
+          bulk_copy_g2s(slot(u) + lane * C::PAGE,
+                        static_cast<const T*>(value ? p.c.v_cache : p.c.k_cache) +
+                            ((size_t)page * p.c.num_kv_heads + x.g) * (D * kPageTokens),
+                        C::PAGE, full);
         ++issued;
         return true;
       };
@@ -334,6 +330,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     constexpr uint32_t id_s = idesc<T>(128, NT / 2), id_o = idesc<T>(128, D);
     const uint64_t aq = smem_desc(base + C::Q, 16 * kTreeRows, 128, kSwizzleNone);
     uint32_t p_count[2] = {0, 0}, segments = 0;
+    uint32_t v_parity = 0;  // a bit per ring slot
     bool ok = true;
     while (ok && walk.next(p, group, x)) {
       const int nt = x.t1 - x.t0;
@@ -360,16 +357,28 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       for (int t = 0; ok && t < nt; ++t) {
         const int b = t & 1, a = NG == 2 ? b : 0;
         const uint32_t u = units + unit_v(t, nt);
-        ok = wait(C::P_READY + b, p_count[b]++ & 1u, kPageStatusTimeout) && wait_unit(u);
+        const uint32_t vs = u % C::STAGES;
+        ok = wait(C::P_READY + b, p_count[b]++ & 1u, kPageStatusTimeout) &&
+             wait(C::V_READY + vs, v_parity >> vs & 1u, kPageStatusTimeout);
         if (!ok) break;
+        v_parity ^= 1u << vs;
         tc_fence_after();
         const uint32_t mask = page_mask[(tiles + t) % kMaskDepth];
         const uint64_t bv = smem_desc(slot(u), 16, 256, kSwizzle32B);
-        for (int j = 0; j < BLK; ++j) {
-          if (!(mask >> j & 1)) continue;
-          mma_ts_if(leader, tmem + C::O(a), tmem + C::S(b) + 8u * j, bv + ((j * C::PAGE) >> 4),
-                    id_o, started[a] ? 1u : 0u);
+        const uint32_t d = tmem + C::O(a), ps = tmem + C::S(b);
+        if (mask == (1u << BLK) - 1u) {
+          mma_ts_if(leader, d, ps, bv, id_o, started[a] ? 1u : 0u);
+#pragma unroll
+          for (int j = 1; j < BLK; ++j)
+            mma_ts_if(leader, d, ps + 8u * j, bv + ((j * C::PAGE) >> 4), id_o, 1u);
           started[a] = true;
+        } else {
+          for (int j = 0; j < BLK; ++j) {
+            if (!(mask >> j & 1)) continue;
+            mma_ts_if(leader, d, ps + 8u * j, bv + ((j * C::PAGE) >> 4), id_o,
+                      started[a] ? 1u : 0u);
+            started[a] = true;
+          }
         }
         mma_commit_if(leader, bar(C::EMPTY + u % C::STAGES));
         mma_commit_if(leader, bar(C::PV_DONE + b));
@@ -381,6 +390,80 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     // every MMA of this warp has finished before TMEM is freed
     mma_commit_if(leader, bar(C::DRAIN));
     wait_drain(bar(C::DRAIN), 0);
+  } else if (warp >= C::FIX && warp < C::FIX + 2) {
+    // ---------------------------------------------- values made operands
+    // Each warp takes half of a tile's rows (a row: one dimension of one page,
+    // 32 bytes).  Rows with bit 2 of the dimension set exchange their halves.
+    const int f = warp - C::FIX;
+    volatile int* flags = reinterpret_cast<volatile int*>(bp + C::ODD);
+    constexpr int ROWS = BLK * D / 2;
+    uint32_t segments = 0;
+    bool ok = true;
+    while (ok && walk.next(p, group, x)) {
+      const int nt = x.t1 - x.t0;
+      const int edge = min(x.s.base, x.s.len);
+      if (lane == 0) flags[2 * (segments % kFlagDepth) + f] = 0;
+      __syncwarp();
+      for (int t = 0; t < nt; ++t) {
+        const uint32_t u = units + unit_v(t, nt);
+        if (!(ok = wait_unit(u))) break;
+        uint8_t* v = bp + C::RING + (u % C::STAGES) * C::UNIT + f * ROWS * 32;
+        // 16-byte pieces of the rows 4 .. 7 of every 8: 8 lanes on 128 bytes
+        uint8_t* at = v + (lane >> 3) * 256 + 128 + (lane & 7) * 16;
+        uint8_t* to = v + (lane >> 3) * 256 + 128 + ((lane & 7) ^ 1) * 16;
+#pragma unroll
+        for (int i = 0; i < ROWS / 32; i += 8) {
+          uint4 e[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (i + k < ROWS / 32) e[k] = *reinterpret_cast<uint4*>(at + (i + k) * 1024);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (i + k < ROWS / 32) *reinterpret_cast<uint4*>(to + (i + k) * 1024) = e[k];
+        }
+        const int p0 = (x.t0 + t) * NT;
+        if (p0 + NT > edge) {
+          // slots past the last token, and non-finite values of drafts, must
+          // not meet a weight of 0
+          __syncwarp();
+          bool odd = false;
+          for (int i = lane; i < ROWS; i += 32) {
+            const int page = (f * ROWS + i) / D, d = (f * ROWS + i) % D;
+            const int q0 = p0 + page * kPageTokens;
+            if (q0 + kPageTokens <= edge) continue;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint4* piece =
+                  reinterpret_cast<uint4*>(v + i * 32 + ((half ^ (d >> 2 & 1)) * 16));
+              uint4 e = *piece;
+              uint32_t* w = reinterpret_cast<uint32_t*>(&e);
+              bool change = false;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int pos = q0 + half * 8 + k;
+                const uint32_t sh = 16 * (k & 1);
+                const bool past = pos >= x.s.len;
+                const bool wild =
+                    pos >= x.s.base && (w[k >> 1] >> sh & Half16<T>::kExp) == Half16<T>::kExp;
+                odd |= wild && !past;
+                if (past || wild) {
+                  w[k >> 1] &= ~(0xffffu << sh);
+                  change = true;
+                }
+              }
+              if (change) *piece = e;
+            }
+          }
+          if (odd) flags[2 * (segments % kFlagDepth) + f] = 1;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::V_READY + u % C::STAGES));
+      }
+      units += 2 * nt;
+      ++segments;
+    }
   } else {
     // ------------------------------------------------------ softmax groups
     // One thread per row.  Control flow around the named barriers is the same
@@ -390,11 +473,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     uint32_t* s_anc = reinterpret_cast<uint32_t*>(bp + C::ANC);
     int* s_parent = reinterpret_cast<int*>(bp + C::PARENT);
     float* s_ml = reinterpret_cast<float*>(bp + C::ML);
-    volatile int* s_nonfinite = reinterpret_cast<volatile int*>(bp + C::NONFINITE);
+    const volatile int* s_odd = reinterpret_cast<const volatile int*>(bp + C::ODD);
     const T* query = static_cast<const T*>(p.query);
     T* out = static_cast<T*>(p.out);
     float* parts = reinterpret_cast<float*>(p.workspace + tree_parts_offset());
-    uint32_t s_count[2] = {0, 0}, pv_count[2] = {0, 0};
+    uint32_t s_count[2] = {0, 0}, pv_count[2] = {0, 0}, segments = 0;
     bool ok = true;
     TreeOpen open{};
     while (walk.next(p, group, x)) {
@@ -406,7 +489,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       const int j = min(r0 + row, x.s.n * group - 1) / group;
       // first position that is not context (every position below it is seen)
       const int edge = min(x.s.base, x.s.len);
-      named_bar_sync(1, C::SOFTMAX);  // the last segment's shared tables are read
+      softmax_barrier(C::SOFTMAX);  // the last segment's shared tables are read
       // the query rows, zeros past the last
       {
         const T* src = query + ((size_t)(x.s.lo + j) * p.num_query_heads + x.g * group +
@@ -421,7 +504,6 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::Q_READY));
-      if (tid == 0) *s_nonfinite = 0;
       const bool drafts = (long long)x.t1 * NT > x.s.base && x.s.n <= kTreeMaxDrafts;
       if (tid == 0 && x.s.n > kTreeMaxDrafts) atomicOr(p.c.status, kPageStatusBadDraft);
       if (drafts) {
@@ -433,7 +515,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           }
           s_parent[a] = up;
         }
-        named_bar_sync(1, C::SOFTMAX);
+        softmax_barrier(C::SOFTMAX);
         const int last = min(r0 + rows - 1, x.s.n * group - 1) / group;
         if (tid <= last - j0) {  // at most 128 drafts have a row in the tile
           uint32_t* mine = s_anc + tid * kAncStride;
@@ -442,7 +524,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           for (int a = j0 + tid; a >= 0; a = s_parent[a]) mine[a >> 5] |= 1u << (a & 31);
         }
       }
-      named_bar_sync(1, C::SOFTMAX);
+      softmax_barrier(C::SOFTMAX);
       const uint32_t* anc = s_anc + (j - j0) * kAncStride;
       const bool live_warp = 32 * (warp & 3) < rows;
       float m = -INFINITY, l = 0.f;
@@ -456,6 +538,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         if (ok && live_warp) {
           tc_fence_after();
           uint32_t s[NT];
+          __syncwarp();
           tmem_ld_cols<NT>(tmem + lanes + C::S(b), s);
           tmem_wait_ld();
 #pragma unroll
@@ -513,6 +596,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             l *= alpha;
           }
           if (t >= NG && __any_sync(0xffffffffu, raise)) {
+            __syncwarp();
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
@@ -537,50 +621,12 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             pk[i] = Half16<T>::pack(a, e);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          __syncwarp();
           tmem_st_cols<NT / 2>(tmem + lanes + C::S(b), pk);
           tmem_wait_st();
         } else if (NG == 1 && t > 0) {
           if (ok) ok = wait(C::PV_DONE + (b ^ 1), pv_count[b ^ 1] & 1u, kPageStatusTimeout);
           ++pv_count[b ^ 1];
-        }
-        if (ok && p0 + NT > edge) {
-          // slots past the last token, and non-finite values of drafts, must
-          // not meet a weight of 0.  Row d of a page is 32 bytes; the swizzle
-          // exchanges its two 16-byte halves where bit 2 of d is set.
-          const uint32_t u = units + unit_v(t, nt);
-          ok = wait_unit(u);
-          if (ok) {
-            uint8_t* v = bp + C::RING + (u % C::STAGES) * C::UNIT;
-            bool odd = false;
-            for (int i = row; i < BLK * D; i += 128) {
-              const int page = i / D, d = i % D, q0 = p0 + page * kPageTokens;
-              if (!(mask >> page & 1u) || q0 + kPageTokens <= edge) continue;
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint4* at = reinterpret_cast<uint4*>(v + page * C::PAGE + d * 32 +
-                                                     ((half ^ (d >> 2 & 1)) * 16));
-                uint4 e = *at;
-                uint32_t* w = reinterpret_cast<uint32_t*>(&e);
-                bool change = false;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const int pos = q0 + half * 8 + k;
-                  const uint32_t sh = 16 * (k & 1);
-                  const bool past = pos >= x.s.len;
-                  const bool wild =
-                      pos >= x.s.base && (w[k >> 1] >> sh & Half16<T>::kExp) == Half16<T>::kExp;
-                  odd |= wild && !past;
-                  if (past || wild) {
-                    w[k >> 1] &= ~(0xffffu << sh);
-                    change = true;
-                  }
-                }
-                if (change) *at = e;
-              }
-            }
-            if (odd) *s_nonfinite = 1;
-            fence_proxy_async_smem();
-          }
         }
         tc_fence_before();
         __syncwarp();
@@ -607,7 +653,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       if (m == -INFINITY && l == 0.f && seen) l = -1.f;
       s_ml[(grp * 2 + 0) * kTreeRows + row] = m;
       s_ml[(grp * 2 + 1) * kTreeRows + row] = l;
-      named_bar_sync(1, C::SOFTMAX);
+      softmax_barrier(C::SOFTMAX);
       // m, l of the row over the groups, and each group's factor
       float gm[NG], gl[NG], f[NG], mm = -INFINITY, ll = 0.f;
       bool nan = false, weightless = false;
@@ -626,7 +672,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       }
       if (nan) ll = __uint_as_float(0x7fc00000u);
       if (mm == -INFINITY && !nan) ll = weightless ? -1.f : 0.f;
-      const bool odd = *s_nonfinite != 0;
+      // (the tile's value products are over, so its values have been looked at)
+      const bool odd = (s_odd[2 * (segments % kFlagDepth)] | s_odd[2 * (segments % kFlagDepth) + 1]) != 0;
       const bool whole = x.whole();
       if (ok && live_warp) {
         tc_fence_after();
@@ -644,6 +691,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           float o[32];
           {
             uint32_t e[NG][32];
+            __syncwarp();
 #pragma unroll
             for (int a = 0; a < NG; ++a) tmem_ld32(tmem + lanes + C::O(a) + c, e[a]);
             tmem_wait_ld();
@@ -706,6 +754,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       }
       units += 2 * nt;
       tiles += nt;
+      ++segments;
     }
     if (tid == 0) {
       if (!ok) open.valid = 0;
@@ -714,6 +763,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   }
 
   // all roles done (or given up, with their async work drained): free TMEM
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -782,18 +832,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
 }
 
 template <int D, typename T>
-cudaError_t launch_dt(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
+cudaError_t launch_dt(const TreeParams& p, cudaStream_t stream) {
   using C = TreeCfg<D>;
-  TreeKernelParams k;
-  k.t = p;
-  const cuuint64_t dims[4] = {kPageTokens, D, (cuuint64_t)p.c.num_kv_heads,
-                              (cuuint64_t)p.c.num_blocks};
-  const cuuint64_t strides[3] = {32, D * 32, (cuuint64_t)p.c.num_kv_heads * D * 32};
-  const cuuint32_t box[4] = {kPageTokens, D, 1, 1}, step[4] = {1, 1, 1, 1};
-  if (enc(&k.vmap, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, p.c.v_cache, dims, strides, box, step,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE))
-    return cudaErrorInvalidValue;
   static bool prepared[kMaxDevices] = {};  // per device: the shared-memory opt-in
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -805,7 +845,7 @@ cudaError_t launch_dt(const TreeParams& p, EncodeTiledFn enc, cudaStream_t strea
     prepared[dev] = true;
   }
   const int grid = std::min(p.c.sm_count, kTreeMaxCtas);
-  tree_kernel<D, T><<<grid, C::THREADS, C::BYTES, stream>>>(k);
+  tree_kernel<D, T><<<grid, C::THREADS, C::BYTES, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, kTreeRows / 32);
@@ -820,17 +860,17 @@ cudaError_t launch_dt(const TreeParams& p, EncodeTiledFn enc, cudaStream_t strea
 }
 
 template <int D>
-cudaError_t launch_d(const TreeParams& p, bool fp16, EncodeTiledFn enc, cudaStream_t stream) {
-  return fp16 ? launch_dt<D, __half>(p, enc, stream) : launch_dt<D, __nv_bfloat16>(p, enc, stream);
+cudaError_t launch_d(const TreeParams& p, bool fp16, cudaStream_t stream) {
+  return fp16 ? launch_dt<D, __half>(p, stream) : launch_dt<D, __nv_bfloat16>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_tree(const TreeParams& p, bool fp16, EncodeTiledFn enc, cudaStream_t stream) {
+cudaError_t launch_tree(const TreeParams& p, bool fp16, cudaStream_t stream) {
   switch (p.c.head_size) {
-    case 64: return launch_d<64>(p, fp16, enc, stream);
-    case 128: return launch_d<128>(p, fp16, enc, stream);
-    case 256: return launch_d<256>(p, fp16, enc, stream);
+    case 64: return launch_d<64>(p, fp16, stream);
+    case 128: return launch_d<128>(p, fp16, stream);
+    case 256: return launch_d<256>(p, fp16, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -2,13 +2,11 @@
 // the C ABI in attn_varlen_api.cu.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstddef>
 #include <cstdint>
 
-#include "attn_varlen_internal.h"
 #include "paged_cache_internal.h"
 
 namespace avp {
@@ -49,6 +47,6 @@ __host__ __device__ constexpr size_t tree_workspace_bytes(int head_size) {
   return tree_parts_offset() + 2 * kTreeMaxCtas * tree_part_floats(head_size) * sizeof(float);
 }
 
-cudaError_t launch_tree(const TreeParams& p, bool fp16, EncodeTiledFn enc, cudaStream_t stream);
+cudaError_t launch_tree(const TreeParams& p, bool fp16, cudaStream_t stream);
 
 }  // namespace avp
