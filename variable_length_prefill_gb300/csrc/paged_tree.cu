@@ -24,24 +24,36 @@
 // P is rounded to the cache type and written to TMEM over its scores, in token
 // order, for the value product.
 //
-// A persistent CTA per SM (NG softmax groups of four warps, a producer, an MMA
-// issuer, two warps that ready the values) takes an equal share of all (sequence, KV head, row tile, key tile)
-// units in that order (paged_walk.cuh), so a long sequence is split over many
-// CTAs without the host knowing a length.  Row tiles that begin and end in one
-// CTA are written to `out`; the others leave unnormalised partial results in
-// the workspace for tree_join_kernel, which adds them in CTA order: results do
-// not depend on timing.
-//
+// A persistent CTA per SM takes an equal share of all (sequence, KV head, row
+// tile, key tile) units in that order (paged_walk.cuh), so a long sequence is
+// split over many CTAs without the host knowing a length.  Row tiles that begin
+// and end in one CTA are written to `out`; the others leave unnormalised partial
+// results in the workspace for tree_join_kernel, which adds them in CTA order:
+// results do not depend on timing.  Warps of a CTA:
+//   producer      walks the CTA's range, publishes its segments (a row tile's
+//                 key tiles in this CTA) and streams their pages through a ring;
+//   two warps     ready the values (below) and build the table of ancestors;
+//   MMA issuer    one elected lane;
+//   softmax       NG groups of four warps, one thread per row.
 // For D <= 128 the two groups take the key tiles in turn, each with its own
 // score buffer, running maximum, sum and accumulator (TMEM: S0 S1 O0 O1), so
 // that one group's exponentials run under the other's products; they are added
-// at the end of the row tile.  For D = 256 one group works on both score
-// buffers (two 256-column accumulators do not fit).
+// at the end of the segment.  For D = 256 one group works on both score buffers
+// (two 256-column accumulators do not fit).
+//
+// Few rows would leave most softmax warps idle while the pages stream.  A tile
+// of at most 64 (32) rows therefore holds each row twice (four times), and each
+// copy takes the weights of its own half (quarter) of the keys, zeros for the
+// others: all four warps share the exponentials, and the copies are added like
+// the groups.  The softmax works on 32 keys at a time, twice over the scores
+// (maximum, then weights), reading them from TMEM again: with all 128 scores of
+// a row in registers the kernel spilled, and its code passed the instruction
+// cache; a tile's softmax took 4000 clocks instead of 1300.
 //
 // A weight of 0 does not silence a NaN or an infinity in the values, so in a
 // tile that holds drafts or slots past the last token, the warps that ready the
-// values clear those slots, and the non-finite values of drafts; the latter are
-// added at the end to the rows that see them.
+// values clear those slots, and the non-finite values of drafts; rows that see
+// one get it back at the end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -61,20 +73,34 @@ constexpr int kMaxDevices = 64;
 constexpr int kAncWords = kTreeMaxDrafts / 32;
 constexpr int kAncStride = kAncWords + 1;  // words between rows of the ancestor table
 constexpr int kMaskDepth = 8;              // key tiles whose page masks are kept
-constexpr int kFlagDepth = 8;              // segments whose flags are kept
+constexpr int kSegDepth = 4;               // published segments
+constexpr int kStageCols = 16;             // columns of an output step
+
+// A CTA's part of one row tile: key tiles [t0, t1) of nt.
+struct Segment {
+  int lo, n;    // packed rows of the sequence
+  int len;      // tokens in the table (0 with too many drafts)
+  int base;     // position of draft 0 (may be negative)
+  int seq, g, mt;
+  int t0, t1, nt;
+  long long u;  // unit number of t0
+  int valid;    // 0: the CTA's range is done
+  int pad;
+  __device__ bool whole() const { return t0 == 0 && t1 == nt; }
+};
 
 template <int D>
 struct TreeCfg {
   static constexpr int NG = D == 256 ? 1 : 2;     // softmax groups
   static constexpr int NT = D == 256 ? 64 : 128;  // keys per tile
   static constexpr int BLK = NT / kPageTokens;    // pages per tile
+  static constexpr int CHUNKS = NT / 32;
   static constexpr uint32_t PAGE = D * kPageTokens * 2;  // bytes of one head's keys (or values)
   static constexpr uint32_t UNIT = BLK * PAGE;           // a key or value tile
   static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? 5 : 4);
   static constexpr int SOFTMAX = 128 * NG;  // softmax threads
   static constexpr int THREADS = SOFTMAX + 128;
-  // Warps past the softmax groups.  The MMA issuer comes last: it then shares
-  // its scheduler with the groups' last warps, which have no rows below 97.
+  // Warps past the softmax groups
   static constexpr int FIX = 4 * NG, PROD = 4 * NG + 2, MMA = 4 * NG + 3;
   // the page masks of tile t are overwritten by tile t + kMaskDepth, whose
   // keys cannot be loaded before t's values are released
@@ -86,22 +112,31 @@ struct TreeCfg {
   // shared memory, from a 1024-byte aligned base
   static constexpr uint32_t RING = 0;
   static constexpr uint32_t Q = RING + STAGES * UNIT;  // [D / 8][128 rows][16 bytes]
-  static constexpr uint32_t ANC = Q + kTreeRows * D * 2;
-  static constexpr uint32_t PARENT = ANC + kTreeRows * kAncStride * 4;
-  static constexpr uint32_t ML = PARENT + kTreeMaxDrafts * 4;  // [NG][2][128] max, sum
-  static constexpr uint32_t MASK = ML + NG * 2 * kTreeRows * 4;
+  // the query rows' place holds the copies' sums at the end of a segment
+  static constexpr uint32_t STAGE = kStageCols * 96 * 4;  // bytes per group
+  static_assert(NG * STAGE <= kTreeRows * D * 2, "stage");
+  static constexpr uint32_t ANC = Q + kTreeRows * D * 2;  // [2][128][kAncStride]
+  static constexpr uint32_t ODD = ANC + 2 * kTreeRows * kAncStride * 4;  // [2][2]
+  static constexpr uint32_t PARENT = ODD + 16;
+  static constexpr uint32_t ML = PARENT + 2 * kTreeMaxDrafts * 4;  // [NG][2][128] max, sum
+  static constexpr uint32_t SEG = ML + NG * 2 * kTreeRows * 4;
+  static_assert(SEG % 8 == 0, "segments");
+  static constexpr uint32_t MASK = SEG + kSegDepth * (uint32_t)sizeof(Segment);
   static constexpr uint32_t BAR = (MASK + kMaskDepth * 4 + 7) & ~7u;
-  // barriers
-  static constexpr int FULL = 0, EMPTY = STAGES, S_FULL = 2 * STAGES, P_READY = S_FULL + 2,
-                       PV_DONE = P_READY + 2, Q_READY = PV_DONE + 2, V_READY = Q_READY + 1,
-                       DRAIN = V_READY + STAGES, NBAR = DRAIN + 1;
+  // Barriers.  A parity wait only tells a phase from the one before it, so a
+  // waiter has to see every phase of its barrier, or know that it is over: keys
+  // (waited for by the MMA issuer) and values (by the value warps) share the
+  // ring's slots and EMPTY, but not the barriers that say they have landed.
+  static constexpr int K_FULL = 0, V_FULL = STAGES, EMPTY = 2 * STAGES, V_READY = 3 * STAGES,
+                       S_FULL = 4 * STAGES,
+                       P_READY = S_FULL + 2, PV_DONE = P_READY + 2, Q_READY = PV_DONE + 2,
+                       ANC_FULL = Q_READY + 1, ANC_EMPTY = ANC_FULL + 2, SEG_FULL = ANC_EMPTY + 2,
+                       SEG_EMPTY = SEG_FULL + kSegDepth, DRAIN = SEG_EMPTY + kSegDepth,
+                       NBAR = DRAIN + 1;
   static constexpr uint32_t TMEM_SLOT = BAR + NBAR * 8;
   static constexpr uint32_t ABORT = TMEM_SLOT + 4;
-  static constexpr uint32_t ODD = ABORT + 4;  // [kFlagDepth][2]
-  static constexpr uint32_t BYTES = ODD + kFlagDepth * 8 + 1024;  // + alignment slack
-  // a segment has at least two units, so the warps that ready values are at
-  // most STAGES / 2 segments ahead of the softmax groups
-  static_assert(kFlagDepth > STAGES / 2, "flag depth");
+  static constexpr uint32_t GO = ABORT + 4;
+  static constexpr uint32_t BYTES = GO + 4 + 1024;  // + alignment slack
   static_assert(BYTES + 512 <= 232448, "one CTA per SM");
 };
 
@@ -134,10 +169,8 @@ __host__ __device__ constexpr uint32_t idesc(uint32_t m, uint32_t n) {
 }
 
 struct SeqInfo {
-  int lo, n;    // packed rows
-  int len;      // tokens in the table (0 with too many drafts)
-  int base;     // position of draft 0 (may be negative)
-  int mts, nt;  // row tiles, key tiles (at least 1)
+  int lo, n, len, base;  // as in Segment
+  int mts, nt;           // row tiles, key tiles (at least 1)
 };
 
 template <int D>
@@ -154,34 +187,36 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int group, int 
   return s;
 }
 
-// A CTA's part of one row tile: key tiles [t0, t1).
-struct Segment {
-  SeqInfo s;
-  int seq, g, mt, t0, t1;
-  long long u;  // unit number of t0
-  __device__ bool whole() const { return t0 == 0 && t1 == s.nt; }
-};
-
-// Every role walks its CTA's range on its own.
+// The producer's walk over its CTA's range.
 template <int D>
 struct Walker {
   long long u, end, off;
-  int seq;
+  int seq, known;  // `s` holds the numbers of sequence `known`
+  SeqInfo s;
   __device__ bool next(const TreeParams& p, int group, Segment& x) {
+    x.valid = 0;
     if (u >= end) return false;
     for (;; ++seq, off = 0) {
       if (seq >= p.c.num_seqs) return false;  // only if the lengths changed under the kernel
-      x.s = seq_info<D>(p, group, seq);
-      const long long units = (long long)x.s.mts * p.c.num_kv_heads * x.s.nt;
-      if (off < units) break;
+      if (known != seq) {
+        s = seq_info<D>(p, group, seq);
+        known = seq;
+      }
+      if (off < (long long)s.mts * p.c.num_kv_heads * s.nt) break;
     }
+    const long long tile = off / s.nt;
+    x.lo = s.lo;
+    x.n = s.n;
+    x.len = s.len;
+    x.base = s.base;
+    x.nt = s.nt;
     x.seq = seq;
-    const long long tile = off / x.s.nt;
-    x.t0 = (int)(off - tile * x.s.nt);
-    x.t1 = (int)min((long long)x.s.nt, x.t0 + (end - u));
-    x.g = (int)(tile / x.s.mts);
-    x.mt = (int)(tile - (long long)x.g * x.s.mts);
+    x.t0 = (int)(off - tile * s.nt);
+    x.t1 = (int)min((long long)s.nt, x.t0 + (end - u));
+    x.g = (int)(tile / s.mts);
+    x.mt = (int)(tile - (long long)x.g * s.mts);
     x.u = u;
+    x.valid = 1;
     u += x.t1 - x.t0;
     off += x.t1 - x.t0;
     return true;
@@ -197,11 +232,12 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
-// Barrier among the softmax warps.  Like the tcgen05 loads and stores it wants
-// the whole warp at once, which lane-dependent branches before it do not promise.
-__device__ __forceinline__ void softmax_barrier(int threads) {
+// Barrier among softmax warps.  Like the tcgen05 loads and stores it wants the
+// whole warp at once, which lane-dependent branches before it do not promise.
+// No warp leaves its loop but by what all of them read behind such a barrier.
+__device__ __forceinline__ void softmax_barrier(int id, int threads) {
   __syncwarp();
-  named_bar_sync(1, threads);
+  named_bar_sync(id, threads);
 }
 
 template <int D, typename T>
@@ -216,13 +252,15 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   uint8_t* bp = smem_raw + (base - raw);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bp + C::ABORT);
   volatile uint32_t* page_mask = reinterpret_cast<volatile uint32_t*>(bp + C::MASK);
+  Segment* segs = reinterpret_cast<Segment*>(bp + C::SEG);
   auto bar = [&](int i) { return base + C::BAR + 8u * (uint32_t)i; };
   auto slot = [&](uint32_t unit) { return base + C::RING + (unit % C::STAGES) * C::UNIT; };
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(bar(C::FULL + s), 1);
+      mbar_init(bar(C::K_FULL + s), 1);
+      mbar_init(bar(C::V_FULL + s), 1);
       mbar_init(bar(C::EMPTY + s), 1);
       mbar_init(bar(C::V_READY + s), 2);
     }
@@ -230,6 +268,12 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       mbar_init(bar(C::S_FULL + b), 1);
       mbar_init(bar(C::P_READY + b), 4);
       mbar_init(bar(C::PV_DONE + b), 1);
+      mbar_init(bar(C::ANC_FULL + b), 2);
+      mbar_init(bar(C::ANC_EMPTY + b), 4 * NG);
+    }
+    for (int s = 0; s < kSegDepth; ++s) {
+      mbar_init(bar(C::SEG_FULL + s), 1);
+      mbar_init(bar(C::SEG_EMPTY + s), 4);  // MMA issuer, value warps, softmax
     }
     mbar_init(bar(C::Q_READY), 4 * NG);
     mbar_init(bar(C::DRAIN), 1);
@@ -252,40 +296,94 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(bp + C::TMEM_SLOT);
   grid_launch_dependents();
-  Walker<D> walk{range.u0, range.u1, range.off, range.seq};
   Segment x;
-  uint32_t units = 0, tiles = 0;  // ring units and key tiles of the segments before this one
-  auto wait = [&](int b, uint32_t parity, int code) -> bool {
-    return __all_sync(0xffffffffu, wait_bounded(bar(b), parity, abort_flag, p.c.status, code));
+  // ring units, key tiles and segments before the current segment
+  uint32_t units = 0, tiles = 0, count = 0;
+  auto wait = [&](int b, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu,
+                      wait_bounded(bar(b), parity, abort_flag, p.c.status, kPageStatusTimeout));
   };
-  auto wait_unit = [&](uint32_t u) -> bool {
-    return wait(C::FULL + u % C::STAGES, (u / C::STAGES) & 1u, kPageStatusTimeout);
+  // wait on a slot's barrier of the array b; `phases` has a bit per slot
+  auto wait_slot = [&](int b, uint32_t s, uint32_t& phases) -> bool {
+    const bool ok = wait(b + s, phases >> s & 1u);
+    phases ^= 1u << s;
+    return ok;
+  };
+  // the next published segment into x; false at the end, or when given up.  Its
+  // place may be used again once every reader has released it.
+  auto next_segment = [&]() -> bool {
+    if (!wait(C::SEG_FULL + count % kSegDepth, (count / kSegDepth) & 1u)) return false;
+    x = segs[count % kSegDepth];
+    return x.valid != 0;
+  };
+  auto release_segment = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::SEG_EMPTY + count % kSegDepth));
+  };
+  // do key tiles of the segment hold drafts that a row may or may not see?
+  auto has_drafts = [&]() -> bool {
+    return (long long)x.t1 * NT > x.base && x.n <= kTreeMaxDrafts;
   };
 
   if (warp == C::PROD) {
     // ------------------------------------------------------------ producer
-    // Page ids come 32 at a time, one read ahead of their use; lane b of the
+    // Page ids come 32 at a time, one read ahead of their use (a segment's
+    // first ones before the last copy of the segment before it); lane b of the
     // warp copies page b of a tile.
     constexpr int TPC = 32 / BLK;  // key tiles per read of ids
+    Walker<D> walk{range.u0, range.u1, range.off, range.seq, -1, {}};
     uint32_t issued = 0;
-    bool ok = true;
-    while (ok && walk.next(p, group, x)) {
+    uint32_t k_phase = 0, v_phase = 0, is_value = 0;  // a bit per slot
+    int ids, next;
+    auto read_ids = [&](const Segment& y, int chunk) -> int {
+      const int i = y.t0 * BLK + chunk * 32 + lane;
+      return chunk * TPC < y.t1 - y.t0 && i < (y.len + kPageTokens - 1) / kPageTokens
+                 ? __ldg(p.block_tables + (size_t)y.seq * p.c.max_blocks + i)
+                 : -1;
+    };
+    // a segment that will be published soon: its page ids, its query rows
+    auto ahead = [&](const Segment& y) {
+      ids = read_ids(y, 0);
+      next = read_ids(y, 1);
+      const int r0 = y.mt * kTreeRows;
+      const int rows = (int)min((long long)kTreeRows, (long long)y.n * group - r0);
+      for (int i = lane; i < rows * (D / 64); i += 32) {
+        const int r = r0 + i / (D / 64), j = r / group;
+        const T* q = static_cast<const T*>(p.query) +
+                     ((size_t)(y.lo + j) * p.num_query_heads + y.g * group + (r - j * group)) * D +
+                     i % (D / 64) * 64;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+      }
+      __syncwarp();
+    };
+    auto publish = [&](const Segment& y) -> bool {
+      const uint32_t s = count % kSegDepth;
+      if (!wait(C::SEG_EMPTY + s, ((count / kSegDepth) & 1u) ^ 1u)) return false;
+      if (lane == 0) {
+        segs[s] = y;
+        mbar_arrive(bar(C::SEG_FULL + s));
+      }
+      __syncwarp();
+      ++count;
+      return true;
+    };
+    bool more = walk.next(p, group, x);
+    if (more) ahead(x);
+    bool ok = publish(x);
+    while (ok && more) {
       const int nt = x.t1 - x.t0;
-      const int pages = (x.s.len + kPageTokens - 1) / kPageTokens;
-      const int32_t* table = p.block_tables + (size_t)x.seq * p.c.max_blocks;
-      auto read_ids = [&](int chunk) -> int {
-        const int i = x.t0 * BLK + chunk * 32 + lane;
-        return chunk * TPC < nt && i < pages ? __ldg(table + i) : -1;
-      };
-      int ids = read_ids(0), next = read_ids(1);
+      const int pages = (x.len + kPageTokens - 1) / kPageTokens;
+      if (lane == 0 && x.n > kTreeMaxDrafts) atomicOr(p.c.status, kPageStatusBadDraft);
       int id[2] = {-1, -1};  // this lane's page of the last two key tiles
-      auto issue = [&](int t, bool value) {
+      auto issue = [&](int t, bool value) -> bool {
         const uint32_t u = issued, s = u % C::STAGES;
-        if (!wait(C::EMPTY + s, ((u / C::STAGES) & 1u) ^ 1u, kPageStatusTimeout)) return false;
+        if (!wait(C::EMPTY + s, ((u / C::STAGES) & 1u) ^ 1u)) return false;
         const int page = t & 1 ? id[1] : id[0];
         const bool there = lane < BLK && page >= 0 && page < p.c.num_blocks;
         const uint32_t mask = __ballot_sync(0xffffffffu, there);
-        const uint32_t full = bar(C::FULL + s);
+        const uint32_t full = bar((value ? C::V_FULL : C::K_FULL) + s);
+        (value ? v_phase : k_phase) ^= 1u << s;
+        is_value = value ? is_value | 1u << s : is_value & ~(1u << s);
         if (lane == 0) {
           if (!value) page_mask[(tiles + t) % kMaskDepth] = mask;
           mbar_arrive_expect_tx(full, __popc(mask) * C::PAGE);
@@ -296,48 +394,57 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
                         static_cast<const T*>(value ? p.c.v_cache : p.c.k_cache) +
                             ((size_t)page * p.c.num_kv_heads + x.g) * (D * kPageTokens),
                         C::PAGE, full);
+        __syncwarp();
         ++issued;
         return true;
       };
-      auto load_k = [&](int t) {
+      auto load_k = [&](int t) -> bool {
         if (t && t % TPC == 0) {
           ids = next;
-          next = read_ids(t / TPC + 1);
+          next = read_ids(x, t / TPC + 1);
         }
         const int mine = __shfl_sync(0xffffffffu, ids, (t % TPC) * BLK + lane % BLK);
         if (t & 1) id[1] = mine; else id[0] = mine;
-        if (lane < BLK && (x.t0 + t) * BLK + lane < pages &&
-            (mine < 0 || mine >= p.c.num_blocks))
+        if (lane < BLK && (x.t0 + t) * BLK + lane < pages && (mine < 0 || mine >= p.c.num_blocks))
           atomicOr(p.c.status, kPageStatusBadBlock);
         return issue(t, false);
       };
       ok = load_k(0) && (nt < 2 || load_k(1));
+      Segment y;
       for (int t = 0; ok && t < nt; ++t) {
+        if (t == nt - 1) {
+          more = walk.next(p, group, y);
+          if (more) ahead(y);
+        }
         ok = issue(t, true);
         if (ok && t + 2 < nt) ok = load_k(t + 2);
       }
+      if (!ok) break;
       tiles += nt;
+      x = y;
+      ok = publish(x);
     }
-    if (!ok) {
-      // let every copy already issued land before the CTA can exit
-      const uint32_t first = issued > (uint32_t)C::STAGES ? issued - C::STAGES : 0;
-      for (uint32_t u = first; u < issued; ++u)
-        wait_drain(bar(C::FULL + u % C::STAGES), (u / C::STAGES) & 1u);
+    // every copy has landed before the CTA can exit (also where others gave up)
+    for (uint32_t s = 0; s < min(issued, (uint32_t)C::STAGES); ++s) {
+      const bool value = is_value >> s & 1u;
+      wait_drain(bar((value ? C::V_FULL : C::K_FULL) + s),
+                 ((value ? v_phase : k_phase) >> s & 1u) ^ 1u);
     }
   } else if (warp == C::MMA) {
     // ---------------------------------------------------------- MMA issuer
     const uint32_t leader = elect_one();
     constexpr uint32_t id_s = idesc<T>(128, NT / 2), id_o = idesc<T>(128, D);
     const uint64_t aq = smem_desc(base + C::Q, 16 * kTreeRows, 128, kSwizzleNone);
-    uint32_t p_count[2] = {0, 0}, segments = 0;
-    uint32_t v_parity = 0;  // a bit per ring slot
+    uint32_t p_phase = 0;  // a bit per score buffer
+    uint32_t k_phase = 0, v_phase = 0;  // a bit per ring slot
     bool ok = true;
-    while (ok && walk.next(p, group, x)) {
+    while (ok && next_segment()) {
+      release_segment();
       const int nt = x.t1 - x.t0;
-      bool started[2] = {false, false};  // the accumulators hold something
-      auto scores = [&](int t) {
+      uint32_t started = 0;  // a bit per accumulator that holds something
+      auto scores = [&](int t) -> bool {
         const uint32_t u = units + unit_k(t);
-        if (!wait_unit(u)) return false;
+        if (!wait_slot(C::K_FULL, u % C::STAGES, k_phase)) return false;
         tc_fence_after();
         const uint64_t bk = smem_desc(slot(u), 256, C::PAGE, kSwizzleNone);
         const uint32_t d = tmem + C::S(t & 1);
@@ -351,41 +458,40 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         mma_commit_if(leader, bar(C::S_FULL + (t & 1)));
         return true;
       };
-      ok = wait(C::Q_READY, segments++ & 1u, kPageStatusTimeout);
+      ok = wait(C::Q_READY, count & 1u);
       if (ok) tc_fence_after();
       ok = ok && scores(0) && (nt < 2 || scores(1));
       for (int t = 0; ok && t < nt; ++t) {
         const int b = t & 1, a = NG == 2 ? b : 0;
-        const uint32_t u = units + unit_v(t, nt);
-        const uint32_t vs = u % C::STAGES;
-        ok = wait(C::P_READY + b, p_count[b]++ & 1u, kPageStatusTimeout) &&
-             wait(C::V_READY + vs, v_parity >> vs & 1u, kPageStatusTimeout);
+        const uint32_t u = units + unit_v(t, nt), vs = u % C::STAGES;
+        ok = wait(C::P_READY + b, p_phase >> b & 1u) && wait_slot(C::V_READY, vs, v_phase);
         if (!ok) break;
-        v_parity ^= 1u << vs;
+        p_phase ^= 1u << b;
         tc_fence_after();
         const uint32_t mask = page_mask[(tiles + t) % kMaskDepth];
         const uint64_t bv = smem_desc(slot(u), 16, 256, kSwizzle32B);
         const uint32_t d = tmem + C::O(a), ps = tmem + C::S(b);
         if (mask == (1u << BLK) - 1u) {
-          mma_ts_if(leader, d, ps, bv, id_o, started[a] ? 1u : 0u);
+          mma_ts_if(leader, d, ps, bv, id_o, started >> a & 1u);
 #pragma unroll
           for (int j = 1; j < BLK; ++j)
             mma_ts_if(leader, d, ps + 8u * j, bv + ((j * C::PAGE) >> 4), id_o, 1u);
-          started[a] = true;
+          started |= 1u << a;
         } else {
+#pragma unroll 1
           for (int j = 0; j < BLK; ++j) {
             if (!(mask >> j & 1)) continue;
-            mma_ts_if(leader, d, ps + 8u * j, bv + ((j * C::PAGE) >> 4), id_o,
-                      started[a] ? 1u : 0u);
-            started[a] = true;
+            mma_ts_if(leader, d, ps + 8u * j, bv + ((j * C::PAGE) >> 4), id_o, started >> a & 1u);
+            started |= 1u << a;
           }
         }
-        mma_commit_if(leader, bar(C::EMPTY + u % C::STAGES));
+        mma_commit_if(leader, bar(C::EMPTY + vs));
         mma_commit_if(leader, bar(C::PV_DONE + b));
         if (t + 2 < nt) ok = scores(t + 2);
       }
       units += 2 * nt;
       tiles += nt;
+      ++count;
     }
     // every MMA of this warp has finished before TMEM is freed
     mma_commit_if(leader, bar(C::DRAIN));
@@ -395,199 +501,263 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     // Each warp takes half of a tile's rows (a row: one dimension of one page,
     // 32 bytes).  Rows with bit 2 of the dimension set exchange their halves.
     const int f = warp - C::FIX;
-    volatile int* flags = reinterpret_cast<volatile int*>(bp + C::ODD);
+    volatile int* s_odd = reinterpret_cast<volatile int*>(bp + C::ODD);
+    int* s_parent = reinterpret_cast<int*>(bp + C::PARENT) + f * kTreeMaxDrafts;
     constexpr int ROWS = BLK * D / 2;
-    uint32_t segments = 0;
+    uint32_t uses = 0;  // segments with drafts before this one
+    uint32_t v_phase = 0;
     bool ok = true;
-    while (ok && walk.next(p, group, x)) {
+    while (ok && next_segment()) {
+      release_segment();
       const int nt = x.t1 - x.t0;
-      const int edge = min(x.s.base, x.s.len);
-      if (lane == 0) flags[2 * (segments % kFlagDepth) + f] = 0;
-      __syncwarp();
+      const int edge = min(x.base, x.len);
+      const bool drafts = has_drafts();
+      const uint32_t a2 = uses & 1u;
+      bool built = false;
       for (int t = 0; t < nt; ++t) {
+        const int p0 = (x.t0 + t) * NT;
+        if (drafts && !built && p0 + NT > edge) {
+          // who sees whom: a bit per draft for every draft that has a row in
+          // the tile, by a walk up the tree (parents are below their children)
+          if (!(ok = wait(C::ANC_EMPTY + a2, ((uses >> 1) & 1u) ^ 1u))) break;
+          if (lane == 0) s_odd[2 * a2 + f] = 0;
+          for (int a = lane; a < x.n; a += 32) {
+            int up = p.parents ? __ldg(p.parents + x.lo + a) : a - 1;
+            if (up < -1 || up >= a) {
+              up = -1;
+              atomicOr(p.c.status, kPageStatusBadDraft);
+            }
+            s_parent[a] = up;
+          }
+          __syncwarp();
+          const int r0 = x.mt * kTreeRows, j0 = r0 / group;
+          const int last =
+              (int)min((long long)r0 + kTreeRows - 1, (long long)x.n * group - 1) / group;
+          uint32_t* table =
+              reinterpret_cast<uint32_t*>(bp + C::ANC) + a2 * kTreeRows * kAncStride;
+          for (int j = j0 + f * 32 + lane; j <= last; j += 64) {
+            uint32_t* mine = table + (j - j0) * kAncStride;
+#pragma unroll
+            for (int w = 0; w < kAncWords; ++w) mine[w] = 0;
+            uint32_t word = 0;
+            int at = j >> 5;
+            for (int a = j; a >= 0; a = s_parent[a]) {
+              if (a >> 5 != at) {
+                mine[at] = word;
+                word = 0;
+                at = a >> 5;
+              }
+              word |= 1u << (a & 31);
+            }
+            mine[at] = word;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::ANC_FULL + a2));
+          built = true;
+        }
         const uint32_t u = units + unit_v(t, nt);
-        if (!(ok = wait_unit(u))) break;
+        if (!(ok = wait_slot(C::V_FULL, u % C::STAGES, v_phase))) break;
         uint8_t* v = bp + C::RING + (u % C::STAGES) * C::UNIT + f * ROWS * 32;
         // 16-byte pieces of the rows 4 .. 7 of every 8: 8 lanes on 128 bytes
         uint8_t* at = v + (lane >> 3) * 256 + 128 + (lane & 7) * 16;
         uint8_t* to = v + (lane >> 3) * 256 + 128 + ((lane & 7) ^ 1) * 16;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < ROWS / 32; i += 8) {
           uint4 e[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (i + k < ROWS / 32) e[k] = *reinterpret_cast<uint4*>(at + (i + k) * 1024);
+          for (int k = 0; k < 8; ++k) e[k] = *reinterpret_cast<uint4*>(at + (i + k) * 1024);
           __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (i + k < ROWS / 32) *reinterpret_cast<uint4*>(to + (i + k) * 1024) = e[k];
+          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(to + (i + k) * 1024) = e[k];
         }
-        const int p0 = (x.t0 + t) * NT;
         if (p0 + NT > edge) {
           // slots past the last token, and non-finite values of drafts, must
           // not meet a weight of 0
           __syncwarp();
-          bool odd = false;
+          uint32_t odd = 0;
+#pragma unroll 1
           for (int i = lane; i < ROWS; i += 32) {
-            const int page = (f * ROWS + i) / D, d = (f * ROWS + i) % D;
-            const int q0 = p0 + page * kPageTokens;
-            if (q0 + kPageTokens <= edge) continue;
+            const int d = i % D, q0 = p0 + (f * ROWS + i) / D * kPageTokens;
+            if (q0 + kPageTokens <= edge || q0 >= x.len) continue;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint4* piece =
-                  reinterpret_cast<uint4*>(v + i * 32 + ((half ^ (d >> 2 & 1)) * 16));
+              uint4* piece = reinterpret_cast<uint4*>(v + i * 32 + ((half ^ (d >> 2 & 1)) * 16));
               uint4 e = *piece;
               uint32_t* w = reinterpret_cast<uint32_t*>(&e);
-              bool change = false;
+              uint32_t change = 0;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int pos = q0 + half * 8 + k;
-                const uint32_t sh = 16 * (k & 1);
-                const bool past = pos >= x.s.len;
-                const bool wild =
-                    pos >= x.s.base && (w[k >> 1] >> sh & Half16<T>::kExp) == Half16<T>::kExp;
-                odd |= wild && !past;
-                if (past || wild) {
-                  w[k >> 1] &= ~(0xffffu << sh);
-                  change = true;
-                }
+              for (int k = 0; k < 4; ++k) {
+                const int pos = q0 + half * 8 + 2 * k;
+                const uint32_t past = (pos >= x.len ? 0xffffu : 0u) |
+                                      (pos + 1 >= x.len ? 0xffff0000u : 0u);
+                const uint32_t draft = (pos >= x.base ? 0xffffu : 0u) |
+                                       (pos + 1 >= x.base ? 0xffff0000u : 0u);
+                constexpr uint32_t kExp2 = Half16<T>::kExp * 0x10001u;
+                const uint32_t wild = __vcmpeq2(w[k] & kExp2, kExp2) & draft & ~past;
+                odd |= wild;
+                change |= w[k] & (wild | past);
+                w[k] &= ~(wild | past);
               }
               if (change) *piece = e;
             }
           }
-          if (odd) flags[2 * (segments % kFlagDepth) + f] = 1;
+          if (odd) s_odd[2 * a2 + f] = 1;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::V_READY + u % C::STAGES));
       }
       units += 2 * nt;
-      ++segments;
+      ++count;
+      if (drafts) ++uses;
     }
   } else {
     // ------------------------------------------------------ softmax groups
-    // One thread per row.  Control flow around the named barriers is the same
-    // in every warp; a warp whose wait gave up only skips its arithmetic.
+    // One thread per row of the tile.  Control flow around the named barriers
+    // is the same in every warp; a warp whose wait gave up only skips its
+    // arithmetic.
     const int grp = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    uint32_t* s_anc = reinterpret_cast<uint32_t*>(bp + C::ANC);
-    int* s_parent = reinterpret_cast<int*>(bp + C::PARENT);
     float* s_ml = reinterpret_cast<float*>(bp + C::ML);
+    volatile int* s_go = reinterpret_cast<volatile int*>(bp + C::GO);
     const volatile int* s_odd = reinterpret_cast<const volatile int*>(bp + C::ODD);
-    const T* query = static_cast<const T*>(p.query);
-    T* out = static_cast<T*>(p.out);
-    float* parts = reinterpret_cast<float*>(p.workspace + tree_parts_offset());
-    uint32_t s_count[2] = {0, 0}, pv_count[2] = {0, 0}, segments = 0;
+    float* stage = reinterpret_cast<float*>(bp + C::Q + grp * C::STAGE);
+    const uint32_t s_tmem[2] = {tmem + lanes + C::S(0), tmem + lanes + C::S(1)};
+    const uint32_t o_tmem = tmem + lanes + C::O(grp);
+    uint32_t s_count = 0, pv_count = 0;  // parities: bit b for buffer b
+    uint32_t uses = 0;
     bool ok = true;
     TreeOpen open{};
-    while (walk.next(p, group, x)) {
+    for (;;) {
+      // The segment is taken by one warp and handed on at the barrier, so that
+      // all go on or stop together.  (All have read the last one's tables.)
+      if (warp == 0) {
+        const bool go = next_segment();
+        if (lane == 0) *s_go = go ? (int)(count % kSegDepth) : -1;
+      }
+      softmax_barrier(1, C::SOFTMAX);
+      if (*s_go < 0) break;
+      if (warp != 0) x = segs[count % kSegDepth];
       const int nt = x.t1 - x.t0;
-      const int rows = (int)min((long long)kTreeRows,
-                                (long long)x.s.n * group - (long long)x.mt * kTreeRows);
       const int r0 = x.mt * kTreeRows;  // row r of the tile is row r0 + r of the sequence
+      const int rows = (int)min((long long)kTreeRows, (long long)x.n * group - r0);
+      // lanes per copy of the rows, and this thread's row and copy
+      const int span = rows <= 32 && C::CHUNKS == 4 ? 32 : (rows <= 64 ? 64 : 128);
+      const int copies = kTreeRows / span, copy = row / span, r = row % span;
       const int j0 = r0 / group;
-      const int j = min(r0 + row, x.s.n * group - 1) / group;
-      // first position that is not context (every position below it is seen)
-      const int edge = min(x.s.base, x.s.len);
-      softmax_barrier(C::SOFTMAX);  // the last segment's shared tables are read
+      const int j = min(r0 + r, x.n * group - 1) / group;
+      const size_t at =
+          ((size_t)(x.lo + j) * p.num_query_heads + x.g * group + (r0 + r - j * group)) * D;
       // the query rows, zeros past the last
       {
-        const T* src = query + ((size_t)(x.s.lo + j) * p.num_query_heads + x.g * group +
-                                (r0 + row - j * group)) * D;
-#pragma unroll 4
-        for (int c = grp; c < D / 8; c += NG) {
-          uint4 e = make_uint4(0, 0, 0, 0);
-          if (row < rows) e = __ldg(reinterpret_cast<const uint4*>(src + c * 8));
-          *reinterpret_cast<uint4*>(bp + C::Q + (c * kTreeRows + row) * 16) = e;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.query) + at);
+        uint4* dst = reinterpret_cast<uint4*>(bp + C::Q) + row;
+#pragma unroll 1
+        for (int c0 = grp; c0 < D / 8; c0 += 8 * NG) {
+          uint4 e[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            e[i] = r < rows && c0 + i * NG < D / 8 ? __ldg(src + c0 + i * NG)
+                                                    : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c0 + i * NG < D / 8) dst[(c0 + i * NG) * kTreeRows] = e[i];
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::Q_READY));
-      const bool drafts = (long long)x.t1 * NT > x.s.base && x.s.n <= kTreeMaxDrafts;
-      if (tid == 0 && x.s.n > kTreeMaxDrafts) atomicOr(p.c.status, kPageStatusBadDraft);
-      if (drafts) {
-        for (int a = tid; a < x.s.n; a += C::SOFTMAX) {
-          int up = p.parents ? __ldg(p.parents + x.s.lo + a) : a - 1;
-          if (up < -1 || up >= a) {
-            up = -1;
-            atomicOr(p.c.status, kPageStatusBadDraft);
-          }
-          s_parent[a] = up;
-        }
-        softmax_barrier(C::SOFTMAX);
-        const int last = min(r0 + rows - 1, x.s.n * group - 1) / group;
-        if (tid <= last - j0) {  // at most 128 drafts have a row in the tile
-          uint32_t* mine = s_anc + tid * kAncStride;
-#pragma unroll
-          for (int w = 0; w < kAncWords; ++w) mine[w] = 0;
-          for (int a = j0 + tid; a >= 0; a = s_parent[a]) mine[a >> 5] |= 1u << (a & 31);
-        }
-      }
-      softmax_barrier(C::SOFTMAX);
-      const uint32_t* anc = s_anc + (j - j0) * kAncStride;
-      const bool live_warp = 32 * (warp & 3) < rows;
+      // first position that is not context (every position below it is seen)
+      const int edge = min(x.base, x.len);
+      const bool drafts = has_drafts();
+      const uint32_t a2 = uses & 1u;
+      const uint32_t* anc = reinterpret_cast<const uint32_t*>(bp + C::ANC) +
+                            (a2 * kTreeRows + (j - j0)) * kAncStride;
+      bool built = false;
       float m = -INFINITY, l = 0.f;
       bool seen = false;
+#pragma unroll 1
       for (int t = grp; t < nt; t += NG) {
         const int b = t & 1;
         const int p0 = (x.t0 + t) * NT;
-        if (ok) ok = wait(C::S_FULL + b, s_count[b] & 1u, kPageStatusTimeout);
-        ++s_count[b];
+        const uint32_t st = b ? s_tmem[1] : s_tmem[0];
+        if (ok) ok = wait(C::S_FULL + b, s_count >> b & 1u);
+        s_count ^= 1u << b;
         const uint32_t mask = page_mask[(tiles + t) % kMaskDepth];
-        if (ok && live_warp) {
+        const bool masked = p0 + NT > edge || mask != (1u << BLK) - 1u;
+        if (masked && drafts && !built) {
+          if (ok) ok = wait(C::ANC_FULL + a2, uses >> 1 & 1u);
+          built = true;
+        }
+        if (NG == 1 && t > 0) {
+          // the accumulator's last product (with two groups, S of this tile
+          // was issued behind it)
+          if (ok) ok = wait(C::PV_DONE + (b ^ 1), pv_count >> (b ^ 1) & 1u);
+          pv_count ^= 1u << (b ^ 1);
+        }
+        if (ok) {
           tc_fence_after();
-          uint32_t s[NT];
-          __syncwarp();
-          tmem_ld_cols<NT>(tmem + lanes + C::S(b), s);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < NT; ++i) asm volatile("" : "+r"(s[i]));
-          // scores the row does not see become -inf; column c of the buffer is
-          // token (c % 8) + 8 half of page (c % (NT / 2)) / 8
-          if (p0 + NT > edge || mask != (1u << BLK) - 1u) {
-#pragma unroll
-            for (int w = 0; w < NT / 32; ++w) {
-              const int q0 = p0 + 32 * w;
-              const int o = q0 - x.s.base;  // draft of the word's first token
-              uint32_t sees = low_bits(edge - q0);
-              if (drafts && o > -32 && o < kTreeMaxDrafts) {
-                if (o < 0) {
-                  sees |= anc[0] << -o;
-                } else {
-                  const int k = o >> 5;
-                  sees |= __funnelshift_r(anc[k], k + 1 < kAncWords ? anc[k + 1] : 0u, o & 31);
-                }
-              }
-              sees &= low_bits(x.s.len - q0);
-              const uint32_t two = mask >> (2 * w);
-              sees &= (two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
-              seen |= sees != 0;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int page = 2 * w + i / 16, half = i % 16 / 8;
-                const int c = half * (NT / 2) + page * 8 + i % 8;
-                if (!(sees >> i & 1u)) s[c] = 0xff800000u;
+          // Keys 32 i .. 32 i + 31 of the tile (pages 2 i, 2 i + 1): their
+          // scores are columns 16 i .. 16 i + 15 (first halves of the pages)
+          // and NT / 2 + 16 i .. + 15 of the buffer, their weights go to
+          // columns 16 i .. 16 i + 15.  s[8 half + 16 page + k] below.
+          auto load = [&](int i, uint32_t (&s)[32]) {
+            __syncwarp();
+            tmem_ld16(st + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&s[0]));
+            tmem_ld16(st + NT / 2 + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&s[16]));
+          };
+          auto sees = [&](int i) -> uint32_t {  // a bit per key
+            const int q0 = p0 + 32 * i;
+            const int o = q0 - x.base;  // draft of the first key
+            uint32_t w = low_bits(edge - q0);
+            if (drafts && o > -32 && o < kTreeMaxDrafts) {
+              if (o < 0) {
+                w |= anc[0] << -o;
+              } else {
+                const int k = o >> 5;
+                w |= __funnelshift_r(anc[k], k + 1 < kAncWords ? anc[k + 1] : 0u, o & 31);
               }
             }
-          } else {
-            seen = true;
-          }
+            w &= low_bits(x.len - q0);
+            const uint32_t two = mask >> (2 * i);
+            return w & ((two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u));
+          };
+          auto hide = [&](int i, uint32_t (&s)[32]) {  // scores not seen become -inf
+            const uint32_t w = sees(i);
+            seen |= w != 0;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              // register k: half k / 16, page k % 16 / 8, token k % 8 + 8 half
+              const int key = k % 16 / 8 * 16 + k / 16 * 8 + k % 8;
+              if (!(w >> key & 1u)) s[k] = 0xff800000u;
+            }
+          };
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto most = [&](const uint32_t (&s)[32]) {
 #pragma unroll
-          for (int i = 0; i < NT; i += 8) {
+            for (int k = 0; k < 32; k += 8)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              mx[q] = fmax3(mx[q], __uint_as_float(s[i + 2 * q]), __uint_as_float(s[i + 2 * q + 1]));
+              for (int q = 0; q < 4; ++q)
+                mx[q] = fmax3(mx[q], __uint_as_float(s[k + 2 * q]), __uint_as_float(s[k + 2 * q + 1]));
+          };
+#pragma unroll 1
+          for (int i = copy; i < C::CHUNKS; i += 2 * copies) {
+            const bool two = i + copies < C::CHUNKS;  // the same in the whole warp
+            uint32_t s0[32], s1[32];
+            load(i, s0);
+            if (two) load(i + copies, s1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(s0[k]), "+r"(s1[k]));
+            if (masked) hide(i, s0);
+            most(s0);
+            if (two) {
+              if (masked) hide(i + copies, s1);
+              most(s1);
+            }
           }
+          if (!masked) seen = true;
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-          // with one group the last product of the accumulator may still run;
-          // with two, S of this tile was issued behind it
-          if (NG == 1 && t > 0) {
-            ok = wait(C::PV_DONE + (b ^ 1), pv_count[b ^ 1] & 1u, kPageStatusTimeout);
-            ++pv_count[b ^ 1];
-            tc_fence_after();
-          }
           // the maximum is only raised by more than 2^8 (weights stay <= 2^8)
           const bool raise = top > m + kRescaleThreshold;
           const float alpha = raise ? ex2(m - top) : 1.f;  // m = -inf: 0
@@ -596,165 +766,219 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             l *= alpha;
           }
           if (t >= NG && __any_sync(0xffffffffu, raise)) {
-            __syncwarp();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
-              tmem_ld32(tmem + lanes + C::O(grp) + c, o);
+              __syncwarp();
+              tmem_ld32(o_tmem + c, o);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(tmem + lanes + C::O(grp) + c, o);
+              tmem_st32(o_tmem + c, o);
             }
             tmem_wait_st();
           }
           const float off = m == -INFINITY ? 0.f : -m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t pk[NT / 2];
+          auto weights = [&](int i, const uint32_t (&s)[32]) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < NT / 2; ++i) {
-            // word i of P: tokens 2 (i % 8) and the next of page i / 8
-            const int c = (i % 8 / 4) * (NT / 2) + i / 8 * 8 + i % 4 * 2;
-            const float a = ex2(fmaf(__uint_as_float(s[c]), p.scale_log2, off));
-            const float e = ex2(fmaf(__uint_as_float(s[c + 1]), p.scale_log2, off));
-            sum[i % 4] += a + e;
-            pk[i] = Half16<T>::pack(a, e);
+            for (int w = 0; w < 16; ++w) {
+              // word w of the weights: keys 2 (w % 8), + 1 of page w / 8
+              const int k = w % 8 / 4 * 16 + w / 8 * 8 + w % 4 * 2;
+              const float a = ex2(fmaf(__uint_as_float(s[k]), p.scale_log2, off));
+              const float e = ex2(fmaf(__uint_as_float(s[k + 1]), p.scale_log2, off));
+              sum[w % 4] += a + e;
+              pk[w] = Half16<T>::pack(a, e);
+            }
+            __syncwarp();
+            tmem_st16(st + 16 * i, pk);
+          };
+#pragma unroll 1
+          for (int i = copy; i < C::CHUNKS; i += 2 * copies) {
+            const bool two = i + copies < C::CHUNKS;
+            uint32_t s0[32], s1[32];
+            load(i, s0);
+            if (two) load(i + copies, s1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(s0[k]), "+r"(s1[k]));
+            if (masked) hide(i, s0);
+            weights(i, s0);
+            if (two) {
+              if (masked) hide(i + copies, s1);
+              weights(i + copies, s1);
+            }
+          }
+          if (copies > 1) {  // the other copies' keys
+            uint32_t zero[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) zero[i] = 0;
+#pragma unroll 1
+            for (int i = 0; i < C::CHUNKS; ++i) {
+              if (i % copies == copy) continue;
+              __syncwarp();
+              tmem_st16(st + 16 * i, zero);
+            }
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          __syncwarp();
-          tmem_st_cols<NT / 2>(tmem + lanes + C::S(b), pk);
           tmem_wait_st();
-        } else if (NG == 1 && t > 0) {
-          if (ok) ok = wait(C::PV_DONE + (b ^ 1), pv_count[b ^ 1] & 1u, kPageStatusTimeout);
-          ++pv_count[b ^ 1];
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::P_READY + b));
       }
-      // the group's last product (with one group also the last of the other
-      // buffer, which the loop has waited for)
-      {
-        const int t = nt - 1 - (NG == 2 && ((nt - 1) & 1) != grp ? 1 : 0);
-        if (NG == 2) {
-          if (t >= 0) {
-            // products of one buffer finish in order: the phases before the
-            // last are known to be over (see above)
-            pv_count[grp] += (t - grp) / 2;
-            if (ok) ok = wait(C::PV_DONE + grp, pv_count[grp] & 1u, kPageStatusTimeout);
-            ++pv_count[grp];
-          }
-        } else {
-          if (ok) ok = wait(C::PV_DONE + (t & 1), pv_count[t & 1] & 1u, kPageStatusTimeout);
-          ++pv_count[t & 1];
+      // the group's last product
+      if (NG == 2) {
+        const int mine = (nt - grp + 1) / 2;  // the group's tiles
+        if (mine > 0) {
+          // products of one buffer finish in order: all but the last are
+          // known to be over (see above)
+          pv_count ^= (uint32_t)((mine - 1) & 1) << grp;
+          if (ok) ok = wait(C::PV_DONE + grp, pv_count >> grp & 1u);
+          pv_count ^= 1u << grp;
         }
+      } else {
+        const int b = (nt - 1) & 1;
+        if (ok) ok = wait(C::PV_DONE + b, pv_count >> b & 1u);
+        pv_count ^= 1u << b;
       }
       // -1 marks a row that sees keys, all with a score of -inf
       if (m == -INFINITY && l == 0.f && seen) l = -1.f;
       s_ml[(grp * 2 + 0) * kTreeRows + row] = m;
       s_ml[(grp * 2 + 1) * kTreeRows + row] = l;
-      softmax_barrier(C::SOFTMAX);
-      // m, l of the row over the groups, and each group's factor
-      float gm[NG], gl[NG], f[NG], mm = -INFINITY, ll = 0.f;
-      bool nan = false, weightless = false;
+      softmax_barrier(1, C::SOFTMAX);
+      if (warp == 0) release_segment();  // all have read it
+      // m, l of the row over groups and copies, and this thread's factors
+      float mm = -INFINITY, ll = 0.f, f[NG];
+      bool nan = false, weightless = false, blank[NG];
+#pragma unroll 1
+      for (int i = r; i < kTreeRows; i += span)
 #pragma unroll
-      for (int a = 0; a < NG; ++a) {
-        gm[a] = s_ml[(a * 2 + 0) * kTreeRows + row];
-        gl[a] = s_ml[(a * 2 + 1) * kTreeRows + row];
-        mm = fmaxf(mm, gm[a]);
-        nan |= !(gl[a] == gl[a]);
-        weightless |= gl[a] == -1.f;
-      }
+        for (int a = 0; a < NG; ++a) mm = fmaxf(mm, s_ml[2 * a * kTreeRows + i]);
+#pragma unroll 1
+      for (int i = r; i < kTreeRows; i += span)
 #pragma unroll
-      for (int a = 0; a < NG; ++a) {
-        f[a] = gm[a] == -INFINITY ? 0.f : ex2(gm[a] - mm);
-        if (f[a] > 0.f) ll += f[a] * gl[a];
-      }
+        for (int a = 0; a < NG; ++a) {
+          const float gm = s_ml[2 * a * kTreeRows + i], gl = s_ml[(2 * a + 1) * kTreeRows + i];
+          const float e = gm == -INFINITY ? 0.f : ex2(gm - mm);
+          if (e > 0.f) ll += e * gl;
+          nan |= !(gl == gl);
+          weightless |= gl == -1.f;
+          if (i == row) {
+            f[a] = e;
+            blank[a] = gm == -INFINITY;
+          }
+        }
       if (nan) ll = __uint_as_float(0x7fc00000u);
       if (mm == -INFINITY && !nan) ll = weightless ? -1.f : 0.f;
-      // (the tile's value products are over, so its values have been looked at)
-      const bool odd = (s_odd[2 * (segments % kFlagDepth)] | s_odd[2 * (segments % kFlagDepth) + 1]) != 0;
+      // (the segment's value products are over, so its values were looked at)
+      const bool odd = drafts && (s_odd[2 * a2] | s_odd[2 * a2 + 1]) != 0;
       const bool whole = x.whole();
-      if (ok && live_warp) {
-        tc_fence_after();
-        const float scale = mm == -INFINITY ? (ll == 0.f ? 0.f : __uint_as_float(0x7fc00000u))
-                                            : 1.f / ll;
-        float* part = parts + (size_t)(2 * blockIdx.x + (x.t0 == 0)) * tree_part_floats(D);
-        if (!whole && grp == 0) {
-          part[D * kTreeRows + row] = mm;
-          part[(D + 1) * kTreeRows + row] = ll;
-        }
-        T* dst = out + ((size_t)(x.s.lo + j) * p.num_query_heads + x.g * group +
-                        (r0 + row - j * group)) * D;
+      float scale = 1.f / ll;
+      if (mm == -INFINITY) scale = ll == 0.f ? 0.f : __uint_as_float(0x7fc00000u);
+      float* part = reinterpret_cast<float*>(p.workspace + tree_parts_offset()) +
+                    (size_t)(2 * blockIdx.x + (x.t0 == 0)) * tree_part_floats(D) + r;
+      if (ok && !whole && row < span && grp == 0) {
+        part[D * kTreeRows] = mm;
+        part[(D + 1) * kTreeRows] = ll;
+      }
+      tc_fence_after();
 #pragma unroll 1
-        for (int c = grp * (D / NG); c < (grp + 1) * (D / NG); c += 32) {
-          float o[32];
-          {
-            uint32_t e[NG][32];
-            __syncwarp();
+      for (int c = grp * (D / NG); c < (grp + 1) * (D / NG); c += kStageCols) {
+        float o[kStageCols];
+        if (ok) {
+          uint32_t e[NG][kStageCols];
+          __syncwarp();
 #pragma unroll
-            for (int a = 0; a < NG; ++a) tmem_ld32(tmem + lanes + C::O(a) + c, e[a]);
-            tmem_wait_ld();
+          for (int a = 0; a < NG; ++a) tmem_ld16(tmem + lanes + C::O(a) + c, e[a]);
+          tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              o[i] = 0.f;
+          for (int i = 0; i < kStageCols; ++i) {
+            o[i] = 0.f;
 #pragma unroll
-              for (int a = 0; a < NG; ++a) {
-                // a group that saw no key of the row may hold anything
-                const float y = __uint_as_float(e[a][i]);
-                if (f[a] != 0.f) o[i] += f[a] * y;
-                else if (gm[a] != -INFINITY && !(y - y == 0.f)) o[i] += y;
-              }
+            for (int a = 0; a < NG; ++a) {
+              // an accumulator that saw no key of the row may hold anything;
+              // a factor of 0 does not silence a NaN or an infinity
+              const float y = __uint_as_float(e[a][i]);
+              o[i] += blank[a] ? 0.f : (f[a] > 0.f ? f[a] * y : (y - y == 0.f ? 0.f : y));
             }
-          }
-          if (odd && drafts && row < rows) {
-            // the non-finite values of the drafts the row sees in this segment
-            const int from = max(x.t0 * NT, max(x.s.base, 0));
-            const int to = (int)min((long long)x.s.len, (long long)x.t1 * NT);
-            for (int pos = from; pos < to; ++pos) {
-              const int a = pos - x.s.base;
-              if (!(anc[a >> 5] >> (a & 31) & 1u)) continue;
-              const int id =
-                  __ldg(p.block_tables + (size_t)x.seq * p.c.max_blocks + pos / kPageTokens);
-              if (id < 0 || id >= p.c.num_blocks) continue;
-              const uint16_t* v = static_cast<const uint16_t*>(p.c.v_cache) +
-                                  (((size_t)id * p.c.num_kv_heads + x.g) * D + c) * kPageTokens +
-                                  pos % kPageTokens;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const uint16_t e = v[i * kPageTokens];
-                if ((e & Half16<T>::kExp) == Half16<T>::kExp) o[i] += Half16<T>::widen(e);
-              }
-            }
-          }
-          if (whole) {
-            if (row < rows) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                uint4 w;
-                w.x = Half16<T>::pack(o[i] * scale, o[i + 1] * scale);
-                w.y = Half16<T>::pack(o[i + 2] * scale, o[i + 3] * scale);
-                w.z = Half16<T>::pack(o[i + 4] * scale, o[i + 5] * scale);
-                w.w = Half16<T>::pack(o[i + 6] * scale, o[i + 7] * scale);
-                *reinterpret_cast<uint4*>(dst + c + i) = w;
-              }
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) part[(c + i) * kTreeRows + row] = o[i];
           }
         }
-        tc_fence_before();
+        if (copies > 1) {
+          const int width = kTreeRows - span;
+          if (row >= span && ok) {
+#pragma unroll
+            for (int i = 0; i < kStageCols; ++i) stage[i * width + row - span] = o[i];
+          }
+          softmax_barrier(2 + grp, 128);
+          if (row < span && ok) {
+            for (int k = r; k < width; k += span)
+#pragma unroll
+              for (int i = 0; i < kStageCols; ++i) o[i] += stage[i * width + k];
+          }
+          softmax_barrier(2 + grp, 128);
+        }
+        if (row >= span || !ok) continue;
+        // The values of drafts were looked at; a copy's weights of 0 for the
+        // keys of the others turn an infinity of the context into a NaN.  Where
+        // either shows, the sum of the non-finite values that the row sees in
+        // this segment is the result (a NaN of the scores is one anyway).
+        float wild = 0.f;
+#pragma unroll
+        for (int i = 0; i < kStageCols; ++i) wild += o[i] - o[i];
+        if (row < rows && !nan && (odd || (copies > 1 && !(wild == 0.f)))) {
+          float sum[kStageCols];
+#pragma unroll
+          for (int i = 0; i < kStageCols; ++i) sum[i] = 0.f;
+          const int to = (int)min((long long)x.len, (long long)x.t1 * NT);
+#pragma unroll 1
+          for (int pos = x.t0 * NT; pos < to; ++pos) {
+            const int a = pos - x.base;
+            if (a >= 0 && !(anc[a >> 5] >> (a & 31) & 1u)) continue;
+            const int id =
+                __ldg(p.block_tables + (size_t)x.seq * p.c.max_blocks + pos / kPageTokens);
+            if (id < 0 || id >= p.c.num_blocks) continue;
+            const uint16_t* v = static_cast<const uint16_t*>(p.c.v_cache) +
+                                (((size_t)id * p.c.num_kv_heads + x.g) * D + c) * kPageTokens +
+                                pos % kPageTokens;
+#pragma unroll
+            for (int i = 0; i < kStageCols; ++i) {
+              const uint16_t e = v[i * kPageTokens];
+              if ((e & Half16<T>::kExp) == Half16<T>::kExp) sum[i] += Half16<T>::widen(e);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kStageCols; ++i)
+            if (!(sum[i] - sum[i] == 0.f)) o[i] = sum[i];
+        }
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < kStageCols; ++i) part[(c + i) * kTreeRows] = o[i];
+        } else if (row < rows) {
+          uint32_t w[kStageCols / 2];
+#pragma unroll
+          for (int i = 0; i < kStageCols / 2; ++i)
+            w[i] = Half16<T>::pack(o[2 * i] * scale, o[2 * i + 1] * scale);
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at + c);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+      if (drafts) {
+        if (lane == 0) mbar_arrive(bar(C::ANC_EMPTY + a2));
+        ++uses;
       }
       if (!whole && x.t0 == 0) {
         const long long used = range.total < gridDim.x ? range.total : gridDim.x;
-        const long long next = x.u + x.s.nt;  // the unit behind the row tile
-        open = {1, x.s.lo, x.s.n, x.g, x.mt,
+        const long long next = x.u + x.nt;  // the unit behind the row tile
+        open = {1, x.lo, x.n, x.g, x.mt,
                 (int)((next * used + range.total - 1) / range.total) - 1, {0, 0}};
       }
-      units += 2 * nt;
       tiles += nt;
-      ++segments;
+      ++count;
     }
     if (tid == 0) {
       if (!ok) open.valid = 0;
