@@ -74,7 +74,10 @@ constexpr int kAncWords = kTreeMaxDrafts / 32;
 constexpr int kAncStride = kAncWords + 1;  // words between rows of the ancestor table
 constexpr int kMaskDepth = 8;              // key tiles whose page masks are kept
 constexpr int kSegDepth = 4;               // published segments
-constexpr int kStageCols = 16;             // columns of an output step
+constexpr int kStageCols = 32;             // columns of an output step
+// A row tile's fixed cost (query rows in, filling the pipeline, output) in key
+// tiles, for the CTAs' equal shares.
+constexpr int kTileOverhead = 3;
 
 // A CTA's part of one row tile: key tiles [t0, t1) of nt.
 struct Segment {
@@ -83,7 +86,7 @@ struct Segment {
   int base;     // position of draft 0 (may be negative)
   int seq, g, mt;
   int t0, t1, nt;
-  long long u;  // unit number of t0
+  long long u;  // first unit of the row tile
   int valid;    // 0: the CTA's range is done
   int pad;
   __device__ bool whole() const { return t0 == 0 && t1 == nt; }
@@ -97,7 +100,7 @@ struct TreeCfg {
   static constexpr int CHUNKS = NT / 32;
   static constexpr uint32_t PAGE = D * kPageTokens * 2;  // bytes of one head's keys (or values)
   static constexpr uint32_t UNIT = BLK * PAGE;           // a key or value tile
-  static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? 5 : 4);
+  static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? 5 : 6);
   static constexpr int SOFTMAX = 128 * NG;  // softmax threads
   static constexpr int THREADS = SOFTMAX + 128;
   // Warps past the softmax groups
@@ -108,14 +111,22 @@ struct TreeCfg {
   // TMEM columns
   __host__ __device__ static constexpr uint32_t S(int b) { return (uint32_t)(b * NT); }
   __host__ __device__ static constexpr uint32_t O(int g) { return (uint32_t)(2 * NT + g * D); }
-  static_assert(2 * NT + NG * D <= 512, "TMEM columns");
+  // The query rows are the products' first operand.  In TMEM, where it has
+  // room for them, they cost no shared-memory reads (D = 256: 38 to 17 clocks
+  // a product); for D = 128 they are in shared memory.
+  static constexpr bool Q_TMEM = D != 128;
+  __host__ __device__ static constexpr uint32_t QT() { return (uint32_t)(2 * NT + NG * D); }
+  static_assert(2 * NT + NG * D + (Q_TMEM ? D / 2 : 0) <= 512, "TMEM columns");
+  static constexpr int QN = D / 8 / NG;           // 16-byte pieces of a row per thread
+  static constexpr int QR = QN < 16 ? QN : 16;    // of them in registers at a time
   // shared memory, from a 1024-byte aligned base
   static constexpr uint32_t RING = 0;
-  static constexpr uint32_t Q = RING + STAGES * UNIT;  // [D / 8][128 rows][16 bytes]
-  // the query rows' place holds the copies' sums at the end of a segment
-  static constexpr uint32_t STAGE = kStageCols * 96 * 4;  // bytes per group
-  static_assert(NG * STAGE <= kTreeRows * D * 2, "stage");
-  static constexpr uint32_t ANC = Q + kTreeRows * D * 2;  // [2][128][kAncStride]
+  // query rows for D = 128, [D / 8][128 rows][16 bytes]; at the end of a segment
+  // the place where copies of a row meet, [NG][kStageCols][128 rows] floats
+  static constexpr uint32_t Q = RING + STAGES * UNIT;
+  static constexpr uint32_t STAGE = kStageCols * kTreeRows * 4;
+  static constexpr uint32_t ANC = Q + NG * STAGE;  // [2][128][kAncStride]
+  static_assert(Q_TMEM || kTreeRows * D * 2 <= NG * STAGE, "query rows");
   static constexpr uint32_t ODD = ANC + 2 * kTreeRows * kAncStride * 4;  // [2][2]
   static constexpr uint32_t PARENT = ODD + 16;
   static constexpr uint32_t ML = PARENT + 2 * kTreeMaxDrafts * 4;  // [NG][2][128] max, sum
@@ -195,31 +206,38 @@ struct Walker {
   SeqInfo s;
   __device__ bool next(const TreeParams& p, int group, Segment& x) {
     x.valid = 0;
-    if (u >= end) return false;
-    for (;; ++seq, off = 0) {
+    while (u < end) {
       if (seq >= p.c.num_seqs) return false;  // only if the lengths changed under the kernel
       if (known != seq) {
         s = seq_info<D>(p, group, seq);
         known = seq;
       }
-      if (off < (long long)s.mts * p.c.num_kv_heads * s.nt) break;
+      const int per = s.nt + kTileOverhead;  // units of a row tile: the overhead, then its tiles
+      if (off >= (long long)s.mts * p.c.num_kv_heads * per) {
+        ++seq;
+        off = 0;
+        continue;
+      }
+      const long long tile = off / per;
+      const int from = (int)(off - tile * per), take = (int)min((long long)per - from, end - u);
+      x.t0 = max(0, from - kTileOverhead);
+      x.t1 = from + take - kTileOverhead;
+      x.u = u - from;
+      u += take;
+      off += take;
+      if (x.t1 <= x.t0) continue;  // a share that ends in the overhead: no tile
+      x.lo = s.lo;
+      x.n = s.n;
+      x.len = s.len;
+      x.base = s.base;
+      x.nt = s.nt;
+      x.seq = seq;
+      x.g = (int)(tile / s.mts);
+      x.mt = (int)(tile - (long long)x.g * s.mts);
+      x.valid = 1;
+      return true;
     }
-    const long long tile = off / s.nt;
-    x.lo = s.lo;
-    x.n = s.n;
-    x.len = s.len;
-    x.base = s.base;
-    x.nt = s.nt;
-    x.seq = seq;
-    x.t0 = (int)(off - tile * s.nt);
-    x.t1 = (int)min((long long)s.nt, x.t0 + (end - u));
-    x.g = (int)(tile / s.mts);
-    x.mt = (int)(tile - (long long)x.g * s.mts);
-    x.u = u;
-    x.valid = 1;
-    u += x.t1 - x.t0;
-    off += x.t1 - x.t0;
-    return true;
+    return false;
   }
 };
 
@@ -289,7 +307,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   const UnitRange range = locate_units<C::THREADS>(
       p.c.num_seqs, blockIdx.x, gridDim.x, scratch, [&](int i) -> long long {
         const SeqInfo s = seq_info<D>(p, group, i);
-        return (long long)s.mts * p.c.num_kv_heads * s.nt;
+        return (long long)s.mts * p.c.num_kv_heads * (s.nt + kTileOverhead);
       });
   tc_fence_before();
   __syncthreads();
@@ -311,10 +329,13 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   };
   // the next published segment into x; false at the end, or when given up.  Its
   // place may be used again once every reader has released it.
+  auto segment_there = [&](uint32_t i) -> bool {
+    return wait(C::SEG_FULL + i % kSegDepth, (i / kSegDepth) & 1u) && segs[i % kSegDepth].valid;
+  };
   auto next_segment = [&]() -> bool {
-    if (!wait(C::SEG_FULL + count % kSegDepth, (count / kSegDepth) & 1u)) return false;
+    if (!segment_there(count)) return false;
     x = segs[count % kSegDepth];
-    return x.valid != 0;
+    return true;
   };
   auto release_segment = [&]() {
     __syncwarp();
@@ -452,8 +473,12 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss_if(leader, d + half * (NT / 2), aq + ((k * 2 * 16 * kTreeRows) >> 4),
-                      bk + ((half * 128 + k * 512) >> 4), id_s, k > 0 ? 1u : 0u);
+            if constexpr (C::Q_TMEM)
+              mma_ts_if(leader, d + half * (NT / 2), tmem + C::QT() + 8 * k,
+                        bk + ((half * 128 + k * 512) >> 4), id_s, k > 0 ? 1u : 0u);
+            else
+              mma_ss_if(leader, d + half * (NT / 2), aq + ((k * 2 * 16 * kTreeRows) >> 4),
+                        bk + ((half * 128 + k * 512) >> 4), id_s, k > 0 ? 1u : 0u);
         mma_commit_if(leader, bar(C::EMPTY + u % C::STAGES));
         mma_commit_if(leader, bar(C::S_FULL + (t & 1)));
         return true;
@@ -628,45 +653,87 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     uint32_t uses = 0;
     bool ok = true;
     TreeOpen open{};
-    for (;;) {
-      // The segment is taken by one warp and handed on at the barrier, so that
-      // all go on or stop together.  (All have read the last one's tables.)
-      if (warp == 0) {
-        const bool go = next_segment();
-        if (lane == 0) *s_go = go ? (int)(count % kSegDepth) : -1;
-      }
-      softmax_barrier(1, C::SOFTMAX);
-      if (*s_go < 0) break;
-      if (warp != 0) x = segs[count % kSegDepth];
-      const int nt = x.t1 - x.t0;
-      const int r0 = x.mt * kTreeRows;  // row r of the tile is row r0 + r of the sequence
-      const int rows = (int)min((long long)kTreeRows, (long long)x.n * group - r0);
-      // lanes per copy of the rows, and this thread's row and copy
-      const int span = rows <= 32 && C::CHUNKS == 4 ? 32 : (rows <= 64 ? 64 : 128);
-      const int copies = kTreeRows / span, copy = row / span, r = row % span;
-      const int j0 = r0 / group;
-      const int j = min(r0 + r, x.n * group - 1) / group;
-      const size_t at =
-          ((size_t)(x.lo + j) * p.num_query_heads + x.g * group + (r0 + r - j * group)) * D;
-      // the query rows, zeros past the last
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.query) + at);
-        uint4* dst = reinterpret_cast<uint4*>(bp + C::Q) + row;
-#pragma unroll 1
-        for (int c0 = grp; c0 < D / 8; c0 += 8 * NG) {
-          uint4 e[8];
+    // lanes per copy of a tile's rows
+    auto span_of = [&](int rows) {
+      return rows <= 32 && C::CHUNKS == 4 ? 32 : (rows <= 64 ? 64 : kTreeRows);
+    };
+    auto rows_of = [&](const Segment& y) {
+      return (int)min((long long)kTreeRows, (long long)y.n * group - (long long)y.mt * kTreeRows);
+    };
+    // element offset of row r of a segment's tile in query and out (rows past
+    // the last: some row of the sequence)
+    auto row_at = [&](const Segment& y, int r) -> size_t {
+      const int r0 = y.mt * kTreeRows, j = min(r0 + r, y.n * group - 1) / group;
+      return ((size_t)(y.lo + j) * p.num_query_heads + y.g * group + (r0 + r - j * group)) * D;
+    };
+    // QR pieces of this thread's query row from piece `first` of its QN on;
+    // zeros past the last row.  Pieces of a row: for TMEM a run per group, for
+    // shared memory every NG-th.
+    auto load_query = [&](const Segment& y, int first, uint4 (&e)[C::QR]) {
+      const int rows = rows_of(y), r = row % span_of(rows);
+      const uint4* src =
+          reinterpret_cast<const uint4*>(static_cast<const T*>(p.query) + row_at(y, r));
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            e[i] = r < rows && c0 + i * NG < D / 8 ? __ldg(src + c0 + i * NG)
-                                                    : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < C::QR; ++i)
+        e[i] = r < rows ? __ldg(src + (C::Q_TMEM ? grp * C::QN + first + i : grp + NG * (first + i)))
+                        : make_uint4(0, 0, 0, 0);
+    };
+    auto store_query = [&](int first, const uint4 (&e)[C::QR]) {
+      if constexpr (C::Q_TMEM) {
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c0 + i * NG < D / 8) dst[(c0 + i * NG) * kTreeRows] = e[i];
+        for (int i = 0; i < C::QR; i += 4) {
+          const uint32_t w[16] = {e[i].x,     e[i].y,     e[i].z,     e[i].w,
+                                  e[i + 1].x, e[i + 1].y, e[i + 1].z, e[i + 1].w,
+                                  e[i + 2].x, e[i + 2].y, e[i + 2].z, e[i + 2].w,
+                                  e[i + 3].x, e[i + 3].y, e[i + 3].z, e[i + 3].w};
+          tmem_st16(tmem + lanes + C::QT() + 4 * (grp * C::QN + first + i), w);
         }
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(bp + C::Q) + row;
+#pragma unroll
+        for (int i = 0; i < C::QR; ++i) dst[(grp + NG * (first + i)) * kTreeRows] = e[i];
       }
-      fence_proxy_async_smem();
+    };
+    auto query_ready = [&]() {
+      if constexpr (C::Q_TMEM) {
+        tmem_wait_st();
+        tc_fence_before();
+      } else {
+        fence_proxy_async_smem();
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::Q_READY));
+    };
+    // A segment is taken by one warp and handed on at a barrier, so that all go
+    // on or stop together.
+    auto take_segment = [&](uint32_t i) {
+      if (warp == 0) {
+        const bool go = segment_there(i);
+        if (lane == 0) *s_go = go ? 1 : 0;
+      }
+    };
+    take_segment(0);
+    softmax_barrier(1, C::SOFTMAX);
+    bool more = *s_go != 0;
+    uint4 query[C::QR];
+    if (more) load_query(segs[0], 0, query);
+    while (more) {
+      x = segs[count % kSegDepth];
+      store_query(0, query);
+#pragma unroll 1
+      for (int i = C::QR; i < C::QN; i += C::QR) {
+        load_query(x, i, query);
+        store_query(i, query);
+      }
+      query_ready();
+      const int nt = x.t1 - x.t0;
+      const int r0 = x.mt * kTreeRows;  // row r of the tile is row r0 + r of the sequence
+      const int rows = rows_of(x);
+      const int span = span_of(rows), copies = kTreeRows / span;
+      const int copy = row / span, r = row % span;  // this thread's copy and row
+      const int j0 = r0 / group;
+      const int j = min(r0 + r, x.n * group - 1) / group;
       // first position that is not context (every position below it is seen)
       const int edge = min(x.base, x.len);
       const bool drafts = has_drafts();
@@ -688,12 +755,6 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         if (masked && drafts && !built) {
           if (ok) ok = wait(C::ANC_FULL + a2, uses >> 1 & 1u);
           built = true;
-        }
-        if (NG == 1 && t > 0) {
-          // the accumulator's last product (with two groups, S of this tile
-          // was issued behind it)
-          if (ok) ok = wait(C::PV_DONE + (b ^ 1), pv_count >> (b ^ 1) & 1u);
-          pv_count ^= 1u << (b ^ 1);
         }
         if (ok) {
           tc_fence_after();
@@ -740,22 +801,31 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
               for (int q = 0; q < 4; ++q)
                 mx[q] = fmax3(mx[q], __uint_as_float(s[k + 2 * q]), __uint_as_float(s[k + 2 * q + 1]));
           };
-#pragma unroll 1
-          for (int i = copy; i < C::CHUNKS; i += 2 * copies) {
-            const bool two = i + copies < C::CHUNKS;  // the same in the whole warp
-            uint32_t s0[32], s1[32];
-            load(i, s0);
-            if (two) load(i + copies, s1);
+          // A copy owns the chunks copy, copy + copies, ...: one, two, or (one
+          // copy of 128 keys) four, of which the second pair stays in registers
+          // between the passes.
+          const bool four = C::CHUNKS / copies == 4, two = C::CHUNKS / copies >= 2;
+          const int i0 = four ? 2 : copy, i1 = four ? 3 : copy + copies;
+          uint32_t s0[32], s1[32];
+          auto load_pair = [&](int a, int b2) {
+            load(a, s0);
+            if (two) load(b2, s1);
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(s0[k]), "+r"(s1[k]));
-            if (masked) hide(i, s0);
-            most(s0);
-            if (two) {
-              if (masked) hide(i + copies, s1);
-              most(s1);
+            if (masked) {
+              hide(a, s0);
+              if (two) hide(b2, s1);
             }
+          };
+          if (four) {
+            load_pair(0, 1);
+            most(s0);
+            most(s1);
           }
+          load_pair(i0, i1);
+          most(s0);
+          if (two) most(s1);
           if (!masked) seen = true;
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
           // the maximum is only raised by more than 2^8 (weights stay <= 2^8)
@@ -766,6 +836,13 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             l *= alpha;
           }
           if (t >= NG && __any_sync(0xffffffffu, raise)) {
+            // With one group the accumulator's last product may still run; with
+            // two, S of this tile was issued behind it.  (Not to wait for a
+            // product loses no phase: S of the next tile is issued behind it.)
+            if (NG == 1) {
+              ok = wait(C::PV_DONE + (b ^ 1), pv_count >> (b ^ 1) & 1u);
+              tc_fence_after();
+            }
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
@@ -794,21 +871,12 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             __syncwarp();
             tmem_st16(st + 16 * i, pk);
           };
-#pragma unroll 1
-          for (int i = copy; i < C::CHUNKS; i += 2 * copies) {
-            const bool two = i + copies < C::CHUNKS;
-            uint32_t s0[32], s1[32];
-            load(i, s0);
-            if (two) load(i + copies, s1);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(s0[k]), "+r"(s1[k]));
-            if (masked) hide(i, s0);
-            weights(i, s0);
-            if (two) {
-              if (masked) hide(i + copies, s1);
-              weights(i + copies, s1);
-            }
+          weights(i0, s0);
+          if (two) weights(i1, s1);
+          if (four) {
+            load_pair(0, 1);
+            weights(0, s0);
+            weights(1, s1);
           }
           if (copies > 1) {  // the other copies' keys
             uint32_t zero[16];
@@ -824,6 +892,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
         }
+        if (NG == 1 && t > 0) pv_count ^= 1u << (b ^ 1);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::P_READY + b));
@@ -847,11 +916,14 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       if (m == -INFINITY && l == 0.f && seen) l = -1.f;
       s_ml[(grp * 2 + 0) * kTreeRows + row] = m;
       s_ml[(grp * 2 + 1) * kTreeRows + row] = l;
+      take_segment(count + 1);
       softmax_barrier(1, C::SOFTMAX);
-      if (warp == 0) release_segment();  // all have read it
+      if (warp == 0) release_segment();  // all have read x
+      more = *s_go != 0;
+      if (more) load_query(segs[(count + 1) % kSegDepth], 0, query);  // in flight from here on
       // m, l of the row over groups and copies, and this thread's factors
       float mm = -INFINITY, ll = 0.f, f[NG];
-      bool nan = false, weightless = false, blank[NG];
+      bool nan = false, weightless = false;
 #pragma unroll 1
       for (int i = r; i < kTreeRows; i += span)
 #pragma unroll
@@ -865,10 +937,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           if (e > 0.f) ll += e * gl;
           nan |= !(gl == gl);
           weightless |= gl == -1.f;
-          if (i == row) {
-            f[a] = e;
-            blank[a] = gm == -INFINITY;
-          }
+          if (i == row) f[a] = gm == -INFINITY ? -1.f : e;  // -1: nothing seen
         }
       if (nan) ll = __uint_as_float(0x7fc00000u);
       if (mm == -INFINITY && !nan) ll = weightless ? -1.f : 0.f;
@@ -879,58 +948,25 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       if (mm == -INFINITY) scale = ll == 0.f ? 0.f : __uint_as_float(0x7fc00000u);
       float* part = reinterpret_cast<float*>(p.workspace + tree_parts_offset()) +
                     (size_t)(2 * blockIdx.x + (x.t0 == 0)) * tree_part_floats(D) + r;
-      if (ok && !whole && row < span && grp == 0) {
+      T* dst = static_cast<T*>(p.out) + row_at(x, r);
+      if (ok && !whole && copy == 0 && grp == 0) {
         part[D * kTreeRows] = mm;
         part[(D + 1) * kTreeRows] = ll;
       }
-      tc_fence_after();
-#pragma unroll 1
-      for (int c = grp * (D / NG); c < (grp + 1) * (D / NG); c += kStageCols) {
-        float o[kStageCols];
-        if (ok) {
-          uint32_t e[NG][kStageCols];
-          __syncwarp();
-#pragma unroll
-          for (int a = 0; a < NG; ++a) tmem_ld16(tmem + lanes + C::O(a) + c, e[a]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < kStageCols; ++i) {
-            o[i] = 0.f;
-#pragma unroll
-            for (int a = 0; a < NG; ++a) {
-              // an accumulator that saw no key of the row may hold anything;
-              // a factor of 0 does not silence a NaN or an infinity
-              const float y = __uint_as_float(e[a][i]);
-              o[i] += blank[a] ? 0.f : (f[a] > 0.f ? f[a] * y : (y - y == 0.f ? 0.f : y));
-            }
-          }
-        }
-        if (copies > 1) {
-          const int width = kTreeRows - span;
-          if (row >= span && ok) {
-#pragma unroll
-            for (int i = 0; i < kStageCols; ++i) stage[i * width + row - span] = o[i];
-          }
-          softmax_barrier(2 + grp, 128);
-          if (row < span && ok) {
-            for (int k = r; k < width; k += span)
-#pragma unroll
-              for (int i = 0; i < kStageCols; ++i) o[i] += stage[i * width + k];
-          }
-          softmax_barrier(2 + grp, 128);
-        }
-        if (row >= span || !ok) continue;
-        // The values of drafts were looked at; a copy's weights of 0 for the
-        // keys of the others turn an infinity of the context into a NaN.  Where
-        // either shows, the sum of the non-finite values that the row sees in
-        // this segment is the result (a NaN of the scores is one anyway).
+      // eight columns of a row: to the output or to the partial results
+      auto put = [&](int c, float (&o)[8]) {
+        // The values of drafts were looked at; weights of 0 (a copy's for the
+        // keys of the others, a factor's) turn an infinity of the context into
+        // a NaN.  Where either shows, the sum of the non-finite values that the
+        // row sees in this segment is the result (a NaN of the scores is one
+        // anyway).
         float wild = 0.f;
 #pragma unroll
-        for (int i = 0; i < kStageCols; ++i) wild += o[i] - o[i];
-        if (row < rows && !nan && (odd || (copies > 1 && !(wild == 0.f)))) {
-          float sum[kStageCols];
+        for (int i = 0; i < 8; ++i) wild += o[i] - o[i];
+        if (r < rows && !nan && (odd || !(wild == 0.f))) {
+          float sum[8];
 #pragma unroll
-          for (int i = 0; i < kStageCols; ++i) sum[i] = 0.f;
+          for (int i = 0; i < 8; ++i) sum[i] = 0.f;
           const int to = (int)min((long long)x.len, (long long)x.t1 * NT);
 #pragma unroll 1
           for (int pos = x.t0 * NT; pos < to; ++pos) {
@@ -943,26 +979,74 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
                                 (((size_t)id * p.c.num_kv_heads + x.g) * D + c) * kPageTokens +
                                 pos % kPageTokens;
 #pragma unroll
-            for (int i = 0; i < kStageCols; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const uint16_t e = v[i * kPageTokens];
               if ((e & Half16<T>::kExp) == Half16<T>::kExp) sum[i] += Half16<T>::widen(e);
             }
           }
 #pragma unroll
-          for (int i = 0; i < kStageCols; ++i)
+          for (int i = 0; i < 8; ++i)
             if (!(sum[i] - sum[i] == 0.f)) o[i] = sum[i];
         }
         if (!whole) {
 #pragma unroll
-          for (int i = 0; i < kStageCols; ++i) part[(c + i) * kTreeRows] = o[i];
-        } else if (row < rows) {
-          uint32_t w[kStageCols / 2];
+          for (int i = 0; i < 8; ++i) part[(c + i) * kTreeRows] = o[i];
+        } else if (r < rows) {
+          *reinterpret_cast<uint4*>(dst + c) = make_uint4(
+              Half16<T>::pack(o[0] * scale, o[1] * scale), Half16<T>::pack(o[2] * scale, o[3] * scale),
+              Half16<T>::pack(o[4] * scale, o[5] * scale), Half16<T>::pack(o[6] * scale, o[7] * scale));
+        }
+      };
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = grp * (D / NG); c < (grp + 1) * (D / NG); c += kStageCols) {
+        float o[kStageCols];
 #pragma unroll
-          for (int i = 0; i < kStageCols / 2; ++i)
-            w[i] = Half16<T>::pack(o[2 * i] * scale, o[2 * i + 1] * scale);
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at + c);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int i = 0; i < kStageCols; ++i) o[i] = 0.f;
+        if (ok) {
+#pragma unroll
+          for (int a = 0; a < NG; ++a) {
+            if (a >= nt) break;  // a group without tiles
+            uint32_t e[kStageCols];
+            __syncwarp();
+            tmem_ld32(tmem + lanes + C::O(a) + c, e);
+            tmem_wait_ld();
+            // an accumulator that saw no key of the row may hold anything
+#pragma unroll
+            for (int i = 0; i < kStageCols; ++i)
+              o[i] = f[a] < 0.f ? o[i] : fmaf(f[a], __uint_as_float(e[i]), o[i]);
+          }
+        }
+        if (copies == 1) {
+          if (ok) {
+#pragma unroll
+            for (int i = 0; i < kStageCols; i += 8) {
+              float w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w[k] = o[i + k];
+              put(c + i, w);
+            }
+          }
+        } else {
+          // the copies of a row meet in shared memory; each puts its share of
+          // the columns
+#pragma unroll
+          for (int i = 0; i < kStageCols; ++i) stage[i * kTreeRows + row] = o[i];
+          softmax_barrier(2 + grp, 128);
+          if (ok) {
+#pragma unroll 1
+            for (int i = copy * (kStageCols / copies); i < (copy + 1) * (kStageCols / copies); i += 8) {
+              float w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float* at = stage + (i + k) * kTreeRows + r;
+                w[k] = at[0] + at[span];
+                if (copies == 4) w[k] += at[2 * span] + at[3 * span];
+              }
+              put(c + i, w);
+            }
+          }
+          softmax_barrier(2 + grp, 128);
         }
       }
       __syncwarp();
@@ -973,12 +1057,14 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       }
       if (!whole && x.t0 == 0) {
         const long long used = range.total < gridDim.x ? range.total : gridDim.x;
-        const long long next = x.u + x.nt;  // the unit behind the row tile
+        const long long next = x.u + x.nt + kTileOverhead;  // the unit behind the row tile
         open = {1, x.lo, x.n, x.g, x.mt,
                 (int)((next * used + range.total - 1) / range.total) - 1, {0, 0}};
       }
       tiles += nt;
       ++count;
+      // what the next segment overwrites is read
+      if (more) softmax_barrier(1, C::SOFTMAX);
     }
     if (tid == 0) {
       if (!ok) open.valid = 0;
