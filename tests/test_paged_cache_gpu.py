@@ -53,6 +53,8 @@ WRITE = [
     ([(i % 40, (i * 7) % 37) for i in range(300)], 5, 64, 0),
     ([(3, 40)] * 3, 20, 128, 0),
     ([(100, 1)] * 700, 2, 128, 0),
+    ([(3, 9000), (0, 1), (40, 17)], 2, 64, 0),  # one far longer than the others
+    ([(i % 20, 1) for i in range(3000)], 3, 64, 0),
 ]
 
 
@@ -307,7 +309,8 @@ def test_fork_then_free_gives_the_pool_back(cuda_lib):
 # -------------------------------------------------------------------- compact
 @pytest.mark.parametrize("blocks,used,hkv,d", [
     (1, 1, 2, 64), (1, 0, 2, 64), (7, 7, 2, 64), (64, 30, 2, 128), (300, 1, 1, 64), (300, 299, 3, 128),
-    (4096, 2000, 1, 64), (4096, 4096, 1, 64), (5000, 4093, 1, 64), (9001, 4100, 1, 64), (100, 50, 8, 256)])
+    (4096, 2000, 1, 64), (4096, 4096, 1, 64), (5000, 4093, 1, 64), (9001, 4100, 1, 64),
+    (16384, 9000, 1, 64), (16385, 16384, 1, 64), (33000, 20000, 1, 64), (100, 50, 8, 256)])
 @pytest.mark.parametrize("place", [False, True])
 def test_compact(cuda_lib, blocks, used, hkv, d, place):
     rng = np.random.default_rng(41)

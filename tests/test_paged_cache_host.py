@@ -80,7 +80,7 @@ def test_fork_arguments(args, code):
     # (k, v, tables, lens, refs, S, Hkv, D, bs, W, blocks, tables_out, refs_out, ws, bytes, stream)
     ((P,) * 5 + (-1, 8, 128, 16, 1, 4, P, P, P, 1 << 20, None), B.ERR_INVALID_ARG),
     ((P,) * 5 + (1, 8, 128, 16, 1, 4, P, None, P, 1 << 20, None), B.ERR_INVALID_ARG),
-    ((P,) * 5 + (1, 8, 128, 16, 1, 4, P, P, P, 4 * 13 - 1, None), B.ERR_WORKSPACE_SMALL),
+    ((P,) * 5 + (1, 8, 128, 16, 1, 4, P, P, P, 4 * 14 - 1, None), B.ERR_WORKSPACE_SMALL),
     ((P,) * 5 + (1, 8, 128, 16, 1, 4, P, P, P + 2, 1 << 20, None), B.ERR_MISALIGNED),
     ((None,) * 5 + (0, 8, 128, 16, 1, 4, None, None, None, 0, None), B.OK),
 ])
@@ -93,7 +93,7 @@ def test_workspace_sizes():
     assert lib.paged_attn_cache_fork_workspace_size(-1, 4) == 0
     assert lib.paged_attn_cache_fork_workspace_size(3, 5) == 4 * 16
     assert lib.paged_attn_cache_compact_workspace_size(-1) == 0
-    assert lib.paged_attn_cache_compact_workspace_size(10) == 4 * 31
+    assert lib.paged_attn_cache_compact_workspace_size(10) == 4 * 32
 
 
 def test_binding_refuses_what_does_not_fit():

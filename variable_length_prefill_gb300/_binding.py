@@ -281,52 +281,69 @@ def chunk_delta_rule_output(q, k, v, h, g, chunk_size=64, scale=None, out=None, 
 
 
 # ------------------------------------------- paged cache and drafted tokens
-# The operators below share their checks: every array on the first tensor's
-# device, int32 arrays contiguous, the two caches of one shape family.
-def _int32(device, **arrays):
+# The operators below take a few microseconds on the GPU, so their checks are
+# written for the host's time: one comparison per property, devices as indexes.
+# A call for another device or stream than the current ones runs again with
+# those made current, so that what it allocates belongs to them.
+def _torch():
+    global _torch_module, _i32, _types, _raw_stream
     import torch
-    for name, (t, shape) in arrays.items():
-        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != device \
-                or tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
+    _torch_module, _i32, _types = torch, torch.int32, (torch.bfloat16, torch.float16)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return torch
+
+
+_torch_module = _i32 = _types = _raw_stream = None
+
+
+def _ints(t, shape, dev, name):
+    if t.dtype is not _i32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on CUDA device {dev}")
 
 
 def _cache(k_cache, v_cache):
-    """(num_blocks, num_kv_heads, head_size, block_size) of a pair of caches."""
-    import torch
-    if k_cache.dim() != 5 or v_cache.dim() != 4:
+    """(num_blocks, num_kv_heads, head_size, block_size, device) of a pair of caches."""
+    if _torch_module is None:
+        _torch()
+    shape = v_cache.shape
+    if len(shape) != 4 or k_cache.dim() != 5:
         raise ValueError("k_cache [B, Hkv, D/8, bs, 8], v_cache [B, Hkv, D, bs]")
-    nb, hkv, d, bs = v_cache.shape
-    if tuple(k_cache.shape) != (nb, hkv, d // 8, bs, 8) or d % 8:
-        raise ValueError(f"k_cache {list(k_cache.shape)} does not fit v_cache {list(v_cache.shape)}")
-    if k_cache.dtype not in (torch.bfloat16, torch.float16) or v_cache.dtype != k_cache.dtype:
+    nb, hkv, d, bs = shape
+    if k_cache.shape != (nb, hkv, d // 8, bs, 8) or d % 8:
+        raise ValueError(f"k_cache {list(k_cache.shape)} does not fit v_cache {list(shape)}")
+    if k_cache.dtype not in _types or v_cache.dtype is not k_cache.dtype:
         raise ValueError("k_cache and v_cache must both be bf16 or both fp16")
-    for t in (k_cache, v_cache):
-        if not t.is_cuda or not t.is_contiguous() or t.device != k_cache.device:
-            raise ValueError("k_cache and v_cache must be contiguous tensors on one CUDA device")
-    return nb, hkv, d, bs
+    dev = k_cache.get_device()
+    if dev < 0 or v_cache.get_device() != dev or not (k_cache.is_contiguous()
+                                                      and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous tensors on one CUDA device")
+    return nb, hkv, d, bs, dev
 
 
-class _On:
-    """The device of a call, and the stream its work and its allocations go to."""
+def _table(block_tables, seq_lens, dev):
+    """(rows, entries of a row) of a block table, its lengths checked."""
+    shape = block_tables.shape
+    if len(shape) != 2:
+        raise ValueError("block_tables must be [S, max_blocks]")
+    _ints(block_tables, shape, dev, "block_tables")
+    _ints(seq_lens, shape[:1], dev, "seq_lens")
+    return shape
 
-    def __init__(self, device, stream):
-        import torch
-        self.device = torch.cuda.device(device)
-        self.stream = torch.cuda.stream(stream) if stream is not None else None
-        self.where = device
 
-    def __enter__(self):
-        import torch
-        self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        return torch.cuda.current_stream(self.where).cuda_stream
+def _elsewhere(dev, stream):
+    """A context that makes the call's device and stream current; None if they are."""
+    cuda = _torch_module.cuda
+    if stream is None:
+        return None if cuda.current_device() == dev else cuda.device(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream belongs to CUDA device {stream.device.index}, the tensors "
+                         f"to {dev}")
+    return cuda.stream(stream)  # makes the stream's device current as well
 
-    def __exit__(self, *a):
-        if self.stream is not None:
-            self.stream.__exit__(*a)
-        return self.device.__exit__(*a)
+
+def _bytes(n, dev):
+    return _torch_module.empty(n, dtype=_torch_module.uint8, device=dev)
 
 
 def _done(rc, where):
@@ -344,25 +361,26 @@ def paged_attn_cache_write(key, value, k_cache, v_cache, block_tables, seq_lens,
     seq_lens int32 [S] counts the new tokens already: the last n of row i are
     the ones written.  The caches are changed in place.
     """
-    nb, hkv, d, bs = _cache(k_cache, v_cache)
-    dev = k_cache.device
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must be [S, max_blocks]")
-    s, w = block_tables.shape
-    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)),
-           cu_seqlens=(cu_seqlens, (s + 1,)))
-    for name, t in (("key", key), ("value", value)):
-        if t.dtype != k_cache.dtype or t.device != dev or t.dim() != 3 \
-                or tuple(t.shape[1:]) != (hkv, d) or t.shape[0] != key.shape[0] \
-                or (t.stride(2) != 1 and t.numel()):
-            raise ValueError(f"{name} must be {k_cache.dtype} [total, {hkv}, {d}] on {dev} with "
-                             "contiguous head elements")
-    with _On(dev, stream) as h:
-        _done(load().paged_attn_cache_write(
-            key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            block_tables.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), s, key.shape[0],
-            hkv, d, bs, w, nb, key.stride(0), key.stride(1), value.stride(0), value.stride(1), h),
-            "paged_attn_cache_write")
+    nb, hkv, d, bs, dev = _cache(k_cache, v_cache)
+    s, w = _table(block_tables, seq_lens, dev)
+    _ints(cu_seqlens, (s + 1,), dev, "cu_seqlens")
+    total = key.shape[0]
+    for t in (key, value):
+        if t.dtype is not k_cache.dtype or t.shape != (total, hkv, d) or t.get_device() != dev \
+                or (t.stride(2) != 1 and total):
+            raise ValueError(f"key and value must be {k_cache.dtype} [total, {hkv}, {d}] on CUDA "
+                             f"device {dev} with contiguous head elements")
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_attn_cache_write(key, value, k_cache, v_cache, block_tables, seq_lens,
+                                          cu_seqlens)
+    kt, kh, _ = key.stride()
+    vt, vh, _ = value.stride()
+    _done((_LIB or load()).paged_attn_cache_write(
+        key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_tables.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), s, total, hkv, d, bs,
+        w, nb, kt, kh, vt, vh, _raw_stream(dev)), "paged_attn_cache_write")
 
 
 def paged_attn_cache_accept(k_cache, v_cache, block_tables, seq_lens, cu_seqlens, accepted,
@@ -374,26 +392,30 @@ def paged_attn_cache_accept(k_cache, v_cache, block_tables, seq_lens, cu_seqlens
     num_accepted int32 [S] says how many.  Returns the rows' new lengths
     (int32 [S], not seq_lens itself).
     """
-    import torch
-    nb, hkv, d, bs = _cache(k_cache, v_cache)
-    dev = k_cache.device
-    if block_tables.dim() != 2 or accepted.dim() != 2:
-        raise ValueError("block_tables must be [S, max_blocks], accepted [S, A]")
-    s, w = block_tables.shape
+    nb, hkv, d, bs, dev = _cache(k_cache, v_cache)
+    s, w = _table(block_tables, seq_lens, dev)
+    if accepted.dim() != 2:
+        raise ValueError("accepted must be [S, A]")
     a = accepted.shape[1]
-    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)),
-           cu_seqlens=(cu_seqlens, (s + 1,)), accepted=(accepted, (s, a)),
-           num_accepted=(num_accepted, (s,)))
-    with _On(dev, stream) as h:
-        if out is None:
-            out = torch.empty_like(seq_lens)
-        _int32(dev, out=(out, (s,)))
-        if s and out.data_ptr() in (seq_lens.data_ptr(), num_accepted.data_ptr()):
+    _ints(cu_seqlens, (s + 1,), dev, "cu_seqlens")
+    _ints(accepted, (s, a), dev, "accepted")
+    _ints(num_accepted, (s,), dev, "num_accepted")
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_attn_cache_accept(k_cache, v_cache, block_tables, seq_lens, cu_seqlens,
+                                           accepted, num_accepted, out)
+    lens = seq_lens.data_ptr()
+    if out is None:
+        out = _torch_module.empty_like(seq_lens)
+    else:
+        _ints(out, (s,), dev, "out")
+        if s and out.data_ptr() in (lens, num_accepted.data_ptr()):
             raise ValueError("out must not be seq_lens or num_accepted")
-        _done(load().paged_attn_cache_accept(
-            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-            cu_seqlens.data_ptr(), accepted.data_ptr(), num_accepted.data_ptr(), s, a, hkv, d, bs,
-            w, nb, out.data_ptr(), h), "paged_attn_cache_accept")
+    _done((_LIB or load()).paged_attn_cache_accept(
+        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), lens,
+        cu_seqlens.data_ptr(), accepted.data_ptr(), num_accepted.data_ptr(), s, a, hkv, d, bs, w,
+        nb, out.data_ptr(), _raw_stream(dev)), "paged_attn_cache_accept")
     return out
 
 
@@ -403,17 +425,21 @@ def paged_attn_cache_free(block_tables, seq_lens, refs, rows, block_size=16, str
     refs int32 [num_blocks] counts the rows that hold each page; rows int32
     [n].  seq_lens and refs are changed in place.
     """
-    dev = block_tables.device
-    if block_tables.dim() != 2 or rows.dim() != 1 or refs.dim() != 1 or not block_tables.is_cuda:
+    if _torch_module is None:
+        _torch()
+    dev = block_tables.get_device()
+    if dev < 0 or rows.dim() != 1 or refs.dim() != 1:
         raise ValueError("block_tables [S, max_blocks], refs [num_blocks], rows [n] on a CUDA device")
-    s, w = block_tables.shape
-    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)),
-           refs=(refs, (refs.numel(),)), rows=(rows, (rows.numel(),)))
-    with _On(dev, stream) as h:
-        _done(load().paged_attn_cache_free(block_tables.data_ptr(), seq_lens.data_ptr(),
-                                           refs.data_ptr(), rows.data_ptr(), rows.numel(), s,
-                                           int(block_size), w, refs.numel(), h),
-              "paged_attn_cache_free")
+    s, w = _table(block_tables, seq_lens, dev)
+    _ints(refs, refs.shape, dev, "refs")
+    _ints(rows, rows.shape, dev, "rows")
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_attn_cache_free(block_tables, seq_lens, refs, rows, block_size)
+    _done((_LIB or load()).paged_attn_cache_free(
+        block_tables.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), rows.data_ptr(),
+        rows.shape[0], s, block_size, w, refs.shape[0], _raw_stream(dev)), "paged_attn_cache_free")
 
 
 def paged_attn_cache_fork(k_cache, v_cache, block_tables, seq_lens, refs, src, dst, stream=None):
@@ -423,23 +449,25 @@ def paged_attn_cache_fork(k_cache, v_cache, block_tables, seq_lens, refs, src, d
     src, dst int32 [n]; every dst row is empty, no src and named once.
     The caches, block_tables, seq_lens and refs are changed in place.
     """
-    import torch
-    nb, hkv, d, bs = _cache(k_cache, v_cache)
-    dev = k_cache.device
-    if block_tables.dim() != 2 or src.dim() != 1:
-        raise ValueError("block_tables must be [S, max_blocks], src and dst [n]")
-    s, w = block_tables.shape
-    n = src.numel()
-    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)), refs=(refs, (nb,)),
-           src=(src, (n,)), dst=(dst, (n,)))
-    lib = load()
+    nb, hkv, d, bs, dev = _cache(k_cache, v_cache)
+    s, w = _table(block_tables, seq_lens, dev)
+    if src.dim() != 1:
+        raise ValueError("src and dst must be [n]")
+    n = src.shape[0]
+    _ints(refs, (nb,), dev, "refs")
+    _ints(src, (n,), dev, "src")
+    _ints(dst, (n,), dev, "dst")
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_attn_cache_fork(k_cache, v_cache, block_tables, seq_lens, refs, src, dst)
+    lib = _LIB or load()
     size = lib.paged_attn_cache_fork_workspace_size(n, s)
-    with _On(dev, stream) as h:
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        _done(lib.paged_attn_cache_fork(
-            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-            refs.data_ptr(), src.data_ptr(), dst.data_ptr(), n, s, hkv, d, bs, w, nb,
-            ws.data_ptr(), size, h), "paged_attn_cache_fork")
+    ws = _bytes(size, dev)
+    _done(lib.paged_attn_cache_fork(
+        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+        refs.data_ptr(), src.data_ptr(), dst.data_ptr(), n, s, hkv, d, bs, w, nb, ws.data_ptr(),
+        size, _raw_stream(dev)), "paged_attn_cache_fork")
 
 
 def paged_attn_cache_compact(k_cache, v_cache, block_tables, seq_lens, refs, out=None, stream=None):
@@ -449,26 +477,28 @@ def paged_attn_cache_compact(k_cache, v_cache, block_tables, seq_lens, refs, out
     which may be the inputs themselves (in place).  The caches are changed in
     place; seq_lens says how many entries of a row are live.
     """
-    import torch
-    nb, hkv, d, bs = _cache(k_cache, v_cache)
-    dev = k_cache.device
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must be [S, max_blocks]")
-    s, w = block_tables.shape
-    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)), refs=(refs, (nb,)))
+    nb, hkv, d, bs, dev = _cache(k_cache, v_cache)
+    s, w = _table(block_tables, seq_lens, dev)
+    _ints(refs, (nb,), dev, "refs")
     if s == 0:
         raise ValueError("block_tables has no row")
-    lib = load()
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_attn_cache_compact(k_cache, v_cache, block_tables, seq_lens, refs, out)
+    if out is None:
+        tables_out, refs_out = _torch_module.empty_like(block_tables), _torch_module.empty_like(refs)
+    else:
+        tables_out, refs_out = out
+        _ints(tables_out, (s, w), dev, "out block_tables")
+        _ints(refs_out, (nb,), dev, "out refs")
+    lib = _LIB or load()
     size = lib.paged_attn_cache_compact_workspace_size(nb)
-    with _On(dev, stream) as h:
-        tables_out, refs_out = out if out is not None else (torch.empty_like(block_tables),
-                                                            torch.empty_like(refs))
-        _int32(dev, out_block_tables=(tables_out, (s, w)), out_refs=(refs_out, (nb,)))
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        _done(lib.paged_attn_cache_compact(
-            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-            refs.data_ptr(), s, hkv, d, bs, w, nb, tables_out.data_ptr(), refs_out.data_ptr(),
-            ws.data_ptr(), size, h), "paged_attn_cache_compact")
+    ws = _bytes(size, dev)
+    _done(lib.paged_attn_cache_compact(
+        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+        refs.data_ptr(), s, hkv, d, bs, w, nb, tables_out.data_ptr(), refs_out.data_ptr(),
+        ws.data_ptr(), size, _raw_stream(dev)), "paged_attn_cache_compact")
     return tables_out, refs_out
 
 
@@ -484,34 +514,37 @@ def paged_attn_tree(query, k_cache, v_cache, block_tables, seq_lens, cu_seqlens,
     itself.  scale: default D^-1/2.  Returns ``out`` (allocated like ``query``
     when not given; rows that no sequence covers are left untouched).
     """
-    import torch
-    nb, hkv, d, bs = _cache(k_cache, v_cache)
-    dev = k_cache.device
-    if block_tables.dim() != 2 or query.dim() != 3:
-        raise ValueError("query must be [total, Hq, D], block_tables [S, max_blocks]")
-    s, w = block_tables.shape
-    total, hq = query.shape[0], query.shape[1]
-    _int32(dev, block_tables=(block_tables, (s, w)), seq_lens=(seq_lens, (s,)),
-           cu_seqlens=(cu_seqlens, (s + 1,)))
+    nb, hkv, d, bs, dev = _cache(k_cache, v_cache)
+    s, w = _table(block_tables, seq_lens, dev)
+    _ints(cu_seqlens, (s + 1,), dev, "cu_seqlens")
+    shape = query.shape
+    dtype = k_cache.dtype
+    for t in (query,) if out is None else (query, out):
+        if t.dtype is not dtype or t.shape != shape or len(shape) != 3 or shape[2] != d \
+                or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"query and out must be contiguous {dtype} tensors [total, Hq, {d}] on "
+                             f"CUDA device {dev}")
+    total, hq, _ = shape
     if parents is not None:
-        _int32(dev, parents=(parents, (total,)))
-    if scale is not None and not 0.0 < scale < float("inf"):
+        _ints(parents, (total,), dev, "parents")
+    if scale is None:
+        scale = 0.0
+    elif not 0.0 < scale < float("inf"):
         raise ValueError("scale must be positive and finite")
-    lib = load()
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_attn_tree(query, k_cache, v_cache, block_tables, seq_lens, cu_seqlens,
+                                   parents, scale or None, out)
+    lib = _LIB or load()
     size = lib.paged_attn_tree_workspace_size(d)
-    with _On(dev, stream) as h:
-        if out is None:
-            out = torch.empty_like(query)
-        for name, t in (("query", query), ("out", out)):
-            if t.dtype != k_cache.dtype or not t.is_contiguous() or t.device != dev \
-                    or tuple(t.shape) != (total, hq, d):
-                raise ValueError(f"{name} must be a contiguous {k_cache.dtype} tensor "
-                                 f"{[total, hq, d]} on {dev}")
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        _done(lib.paged_attn_tree(
-            query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-            seq_lens.data_ptr(), cu_seqlens.data_ptr(),
-            parents.data_ptr() if parents is not None else None, s, total, hq, hkv, d, bs, w, nb,
-            float(scale or 0.0), 1 if query.dtype == torch.float16 else 0, out.data_ptr(),
-            ws.data_ptr(), size, h), "paged_attn_tree")
+    ws = _bytes(size, dev)
+    if out is None:
+        out = _torch_module.empty_like(query)
+    _done(lib.paged_attn_tree(
+        query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), cu_seqlens.data_ptr(),
+        None if parents is None else parents.data_ptr(), s, total, hq, hkv, d, bs, w, nb, scale,
+        1 if dtype is _types[1] else 0, out.data_ptr(), ws.data_ptr(), size, _raw_stream(dev)),
+        "paged_attn_tree")
     return out

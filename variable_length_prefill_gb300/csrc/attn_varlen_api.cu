@@ -686,7 +686,7 @@ int paged_attn_cache_fork(void* k_cache, void* v_cache, int32_t* block_tables, i
 
 size_t paged_attn_cache_compact_workspace_size(int num_blocks) {
   if (num_blocks < 0) return 0;
-  return 4 * (1 + 3 * (size_t)num_blocks);
+  return 4 * (2 + 3 * (size_t)num_blocks);
 }
 
 int paged_attn_cache_compact(void* k_cache, void* v_cache, const int32_t* block_tables,
@@ -712,9 +712,9 @@ int paged_attn_cache_compact(void* k_cache, void* v_cache, const int32_t* block_
   p.refs = refs;
   p.block_tables_out = block_tables_out;
   p.refs_out = refs_out;
-  p.moves = static_cast<int32_t*>(workspace);
-  p.remap = p.moves + 1;
-  p.from = p.remap + num_blocks;
+  p.head = static_cast<int32_t*>(workspace);
+  p.number = p.head + 2;
+  p.from = p.number + num_blocks;
   p.to = p.from + num_blocks;
   return map_cuda(avp::launch_cache_compact(p, stream));
 }

@@ -36,117 +36,123 @@ __device__ __forceinline__ NewTokens new_tokens(const int32_t* __restrict__ cu,
 // --------------------------------------------------------------------- write
 // Bound by HBM: every new element is read once and written once.  A unit is
 // one page of one sequence for a group of heads, so that the tokens of a page
-// meet in one CTA: the value cache is token-fastest, and a thread that holds
-// 8 tokens of 8 dimensions turns them over in registers and writes whole
-// 16-byte pieces of 8 tokens (32 bytes with its neighbour).  Keys keep their
-// 8-element pieces: 16 lanes write 16 tokens of a piece, 256 bytes in a row.
+// meet in one CTA: the value cache is token-fastest, and a thread that holds 8
+// tokens of 8 dimensions turns them over in registers and writes whole 16-byte
+// pieces of 8 tokens (32 bytes with its neighbour).  Keys keep their 8-element
+// pieces: 16 lanes write 16 tokens of a piece, 256 bytes in a row.  Eight loads
+// a thread are out at a time, with four CTAs on an SM.
 constexpr int kWriteThreads = 256;
+constexpr int kWriteKeys = 8;  // key pieces a thread moves per page of a full head group
 
-struct WriteUnit {
-  int first, pages;  // pages [first, first + pages) of the sequence take new tokens
+struct WritePages {
+  int begin, end;    // positions that are written
+  int first, pages;  // their pages
 };
 
-__device__ __forceinline__ WriteUnit write_pages(const NewTokens& t, int max_blocks) {
-  const long long cap = (long long)max_blocks * kPage;
-  const int begin = max(t.len - t.n, 0);
-  const int end = (int)min((long long)t.len, cap);
-  WriteUnit w;
-  w.first = begin / kPage;
-  w.pages = t.n > 0 && end > begin ? (end - 1) / kPage - w.first + 1 : 0;
+__device__ __forceinline__ WritePages write_pages(const NewTokens& t, int max_blocks) {
+  WritePages w;
+  w.begin = max(t.len - t.n, 0);
+  w.end = (int)min((long long)t.len, (long long)max_blocks * kPage);
+  w.first = w.begin / kPage;
+  w.pages = t.n > 0 && w.end > w.begin ? (w.end - 1) / kPage - w.first + 1 : 0;
   return w;
 }
 
-__global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(
+__global__ void __launch_bounds__(kWriteThreads, 4) cache_write_kernel(
     const __grid_constant__ CacheWriteParams p, int head_group) {
   __shared__ UnitScratch scratch;
   const int groups = (p.c.num_kv_heads + head_group - 1) / head_group;
-  auto count = [&](int i) -> long long {
-    return (long long)write_pages(new_tokens(p.cu, p.seq_lens, i, p.total_tokens), p.c.max_blocks)
-               .pages * groups;
-  };
-  const UnitRange r =
-      locate_units<kWriteThreads>(p.c.num_seqs, blockIdx.x, gridDim.x, scratch, count);
+  const UnitRange range = locate_units<kWriteThreads>(
+      p.c.num_seqs, blockIdx.x, gridDim.x, scratch, [&](int i) -> long long {
+        const NewTokens t = new_tokens(p.cu, p.seq_lens, i, p.total_tokens);
+        return (long long)write_pages(t, p.c.max_blocks).pages * groups;
+      });
   const int tid = threadIdx.x;
-  const int pieces = p.c.head_size / 8;  // 16-byte pieces of a head's elements
+  const int pieces = p.c.head_size / 8;  // 16-byte pieces of a head's elements, a power of two
+  const int shift = __ffs(pieces) - 1;
   const uint16_t* key = static_cast<const uint16_t*>(p.key);
   const uint16_t* value = static_cast<const uint16_t*>(p.value);
   uint16_t* kc = static_cast<uint16_t*>(p.c.k_cache);
   uint16_t* vc = static_cast<uint16_t*>(p.c.v_cache);
-  int seq = r.seq;
-  long long off = r.off;
-  for (long long u = r.u0; u < r.u1; ++u, ++off) {
-    NewTokens t;
-    WriteUnit w;
-    for (;; ++seq, off = 0) {
+  // a thread's items: values (head, 8 dimensions, 8 slots), one; keys (head,
+  // piece, slot), kWriteKeys
+  const int half = tid & 1, vpiece = (tid >> 1) & (pieces - 1), vh = tid >> (1 + shift);
+  const int slot = tid & (kPage - 1);
+  int seq = range.seq;
+  long long off = range.off;
+  NewTokens t;
+  WritePages w;
+  bool known = false;
+  for (long long u = range.u0; u < range.u1; ++u, ++off) {
+    for (;; ++seq, off = 0, known = false) {
       if (seq >= p.c.num_seqs) return;  // only if the lengths changed under the kernel
-      t = new_tokens(p.cu, p.seq_lens, seq, p.total_tokens);
-      w = write_pages(t, p.c.max_blocks);
+      if (!known) {
+        t = new_tokens(p.cu, p.seq_lens, seq, p.total_tokens);
+        w = write_pages(t, p.c.max_blocks);
+        known = true;
+      }
       if (off < (long long)w.pages * groups) break;
     }
-    const int page = w.first + (int)(off / groups);
-    const int g0 = (int)(off % groups) * head_group;
+    const int page = w.first + (int)(off / groups), g0 = (int)(off % groups) * head_group;
     const int heads = min(head_group, p.c.num_kv_heads - g0);
-    if (tid == 0 && t.len > p.c.max_blocks * (long long)kPage)
-      atomicOr(p.c.status, kPageStatusBadBlock);
     const int id = __ldg(p.block_tables + (size_t)seq * p.c.max_blocks + page);
+    if (tid == 0 && t.len > w.end) atomicOr(p.c.status, kPageStatusBadBlock);
     if (id < 0 || id >= p.c.num_blocks) {
       if (tid == 0) atomicOr(p.c.status, kPageStatusBadBlock);
       continue;
     }
     // slots [s0, s1) of the page take packed rows row0 + slot
-    const int base = t.len - t.n;
-    const int s0 = max(base - page * kPage, 0), s1 = min(t.len - page * kPage, kPage);
-    const long long row0 = (long long)t.lo + page * kPage - base;
+    const int s0 = max(w.begin - page * kPage, 0), s1 = min(w.end - page * kPage, kPage);
+    const long long row0 = (long long)t.lo + page * kPage - (t.len - t.n);
     const size_t head0 = (size_t)id * p.c.num_kv_heads + g0;
-    // keys: item = (head, piece, slot), slots fastest
-    const int kitems = heads * pieces * kPage;
-#pragma unroll 4
-    for (int x = tid; x < kitems; x += kWriteThreads) {
-      const int slot = x % kPage, piece = (x / kPage) % pieces, h = x / (kPage * pieces);
-      if (slot < s0 || slot >= s1) continue;
-      const uint4 e = *reinterpret_cast<const uint4*>(key + (row0 + slot) * p.key_token +
-                                                      (g0 + h) * p.key_head + piece * 8);
-      *reinterpret_cast<uint4*>(kc + ((head0 + h) * pieces + piece) * (kPage * 8) + slot * 8) = e;
+    if (slot >= s0 && slot < s1) {
+      const uint16_t* src = key + (row0 + slot) * p.key_token + (long long)g0 * p.key_head;
+      uint16_t* dst = kc + head0 * pieces * (kPage * 8) + slot * 8;
+      const int x0 = tid / kPage, items = heads * pieces;
+      uint4 e[kWriteKeys];
+#pragma unroll
+      for (int i = 0; i < kWriteKeys; ++i) {
+        const int x = x0 + i * (kWriteThreads / kPage);
+        if (x < items)
+          e[i] = *reinterpret_cast<const uint4*>(src + (x >> shift) * p.key_head +
+                                                 (x & (pieces - 1)) * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < kWriteKeys; ++i) {
+        const int x = x0 + i * (kWriteThreads / kPage);
+        if (x < items) *reinterpret_cast<uint4*>(dst + x * (kPage * 8)) = e[i];
+      }
     }
-    // values: item = (head, 8 dimensions, 8 slots)
-    const int vitems = heads * pieces * 2;
-    for (int x = tid; x < vitems; x += kWriteThreads) {
-      const int half = x & 1, piece = (x >> 1) % pieces, h = x / (2 * pieces);
-      const int lo = max(s0 - half * 8, 0), hi = min(s1 - half * 8, 8);
-      if (lo >= hi) continue;
+    const int lo = max(s0 - half * 8, 0), hi = min(s1 - half * 8, 8);
+    if (vh >= heads || lo >= hi) continue;
+    const uint16_t* src = value + (row0 + half * 8) * p.value_token +
+                          (long long)(g0 + vh) * p.value_head + vpiece * 8;
+    uint16_t* dst = vc + ((head0 + vh) * p.c.head_size + vpiece * 8) * kPage + half * 8;
+    if (hi - lo == 8) {
       uint32_t e[8][4];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (i >= lo && i < hi) {
-          const uint4 v = *reinterpret_cast<const uint4*>(
-              value + (row0 + half * 8 + i) * p.value_token + (g0 + h) * p.value_head + piece * 8);
-          e[i][0] = v.x, e[i][1] = v.y, e[i][2] = v.z, e[i][3] = v.w;
-        } else {
-          e[i][0] = e[i][1] = e[i][2] = e[i][3] = 0;
-        }
+        const uint4 v = *reinterpret_cast<const uint4*>(src + i * p.value_token);
+        e[i][0] = v.x, e[i][1] = v.y, e[i][2] = v.z, e[i][3] = v.w;
       }
-      uint16_t* dst =
-          vc + ((head0 + h) * p.c.head_size + piece * 8) * kPage + half * 8;
-      if (hi - lo == 8) {
 #pragma unroll
-        for (int d = 0; d < 8; ++d) {
-          // tokens 2 j, 2 j + 1 of dimension d in one word
-          const uint32_t sel = d & 1 ? 0x7632u : 0x5410u;
-          uint4 o;
-          o.x = __byte_perm(e[0][d >> 1], e[1][d >> 1], sel);
-          o.y = __byte_perm(e[2][d >> 1], e[3][d >> 1], sel);
-          o.z = __byte_perm(e[4][d >> 1], e[5][d >> 1], sel);
-          o.w = __byte_perm(e[6][d >> 1], e[7][d >> 1], sel);
-          *reinterpret_cast<uint4*>(dst + d * kPage) = o;
-        }
-      } else {
+      for (int d = 0; d < 8; ++d) {
+        // tokens 2 j, 2 j + 1 of dimension d in one word
+        const uint32_t sel = d & 1 ? 0x7632u : 0x5410u;
+        uint4 o;
+        o.x = __byte_perm(e[0][d >> 1], e[1][d >> 1], sel);
+        o.y = __byte_perm(e[2][d >> 1], e[3][d >> 1], sel);
+        o.z = __byte_perm(e[4][d >> 1], e[5][d >> 1], sel);
+        o.w = __byte_perm(e[6][d >> 1], e[7][d >> 1], sel);
+        *reinterpret_cast<uint4*>(dst + d * kPage) = o;
+      }
+    } else {
+#pragma unroll 1
+      for (int i = lo; i < hi; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src + i * p.value_token);
+        const uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i < lo || i >= hi) continue;
-#pragma unroll
-          for (int d = 0; d < 8; ++d)
-            dst[d * kPage + i] = (uint16_t)(e[i][d >> 1] >> (16 * (d & 1)));
-        }
+        for (int d = 0; d < 8; ++d) dst[d * kPage + i] = (uint16_t)(e[d >> 1] >> (16 * (d & 1)));
       }
     }
   }
@@ -311,6 +317,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(
     const __grid_constant__ CacheForkParams p) {
   __shared__ int s_warp[32];
   const int tid = threadIdx.x;
+  grid_launch_dependents();
   for (int r = tid; r < p.c.num_seqs; r += kPlanThreads) {
     p.owner[r] = INT_MAX;
     p.is_src[r] = 0;
@@ -392,6 +399,7 @@ __device__ __forceinline__ void copy_pieces(const uint4* __restrict__ src, uint4
 __global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(
     const __grid_constant__ CacheForkParams p) {
   const int j = blockIdx.x, part = blockIdx.y;
+  grid_wait_prerequisite();
   const int fresh = p.state[j];
   if (fresh == kRefused) return;
   const int s = __ldg(p.src + j), d = __ldg(p.dst + j);
@@ -435,90 +443,139 @@ __global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(
 // A plan (one CTA) counts the used pages, U, and lists the moves: the i-th
 // lowest hole below U receives the i-th highest used page.  Both indexes
 // follow from one scan u(p) = used pages below p: a hole p is number p - u(p),
-// a used page p >= U is number U - u(p) - 1.  Then pages are copied and table
-// entries renamed side by side.
+// a used page p >= U is number U - u(p) - 1.  Then pages are copied, counts
+// moved and table entries renamed side by side: an entry below U stays, one at
+// or past it asks its page's number i (checked against the list, so an entry
+// that no count backs stays as it is).
+//
+// The copies are bound by HBM; the plan is bound by latency, so each of its
+// threads takes 16 pages at a time, in registers between the count and the
+// scan where the pool has at most 16384.
 constexpr int kCompactThreads = 256;
 constexpr int kPieceGroup = 1024;  // 16-byte pieces of a page one CTA copies at a time
+constexpr int kPlanPages = 16;     // pages a plan thread takes at a time
+
+__device__ __forceinline__ void load_counts(const int32_t* refs, long long b, int blocks,
+                                            int (&ref)[kPlanPages]) {
+  if ((reinterpret_cast<uintptr_t>(refs) & 15u) == 0 && b + kPlanPages <= blocks) {
+#pragma unroll
+    for (int i = 0; i < kPlanPages; i += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(refs + b + i);
+      ref[i] = v.x, ref[i + 1] = v.y, ref[i + 2] = v.z, ref[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPlanPages; ++i) ref[i] = b + i < blocks ? refs[b + i] : 0;
+  }
+}
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(
     const __grid_constant__ CacheCompactParams p) {
   __shared__ int s_warp[32];
   const int tid = threadIdx.x, blocks = p.c.num_blocks;
-  int mine = 0;
-  for (long long b = tid; b < blocks; b += kPlanThreads) mine += p.refs[b] > 0;
+  constexpr int kStep = kPlanPages * kPlanThreads;
+  grid_launch_dependents();
+  int ref[kPlanPages], mine = 0;
+  for (long long b0 = 0; b0 < blocks; b0 += kStep) {
+    load_counts(p.refs, b0 + kPlanPages * tid, blocks, ref);
+#pragma unroll
+    for (int i = 0; i < kPlanPages; ++i) mine += ref[i] > 0;
+  }
   int used;
-  block_exclusive(mine, used, s_warp);
+  int below = block_exclusive(mine, used, s_warp);  // used pages of lower threads
+  if (tid == 0) {
+    p.head[0] = 0;
+    p.head[1] = used;
+  }
+  __syncthreads();
   int before = 0;  // used pages below b0
-  for (long long b0 = 0; b0 < blocks; b0 += 4 * kPlanThreads) {
-    const long long b = b0 + 4 * tid;
-    int ref[4], n = 0;
+  for (long long b0 = 0; b0 < blocks; b0 += kStep) {
+    const long long b = b0 + kPlanPages * tid;
+    if (blocks > kStep) {
+      load_counts(p.refs, b, blocks, ref);
+      int n = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ref[i] = b + i < blocks ? p.refs[b + i] : 0;
-      n += ref[i] > 0;
+      for (int i = 0; i < kPlanPages; ++i) n += ref[i] > 0;
+      int total;
+      below = before + block_exclusive(n, total, s_warp);
+      before += total;
     }
-    int total;
-    int u = before + block_exclusive(n, total, s_warp);
+    int u = below;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (b + i >= blocks) break;
+    for (int i = 0; i < kPlanPages; ++i) {
       const int id = (int)b + i;
+      if (b + i >= blocks) break;
+      if (id == used) p.head[0] = used - u;  // holes below `used`
       if (ref[i] <= 0 && id < used) p.to[id - u] = id;
-      if (ref[i] > 0 && id >= used) p.from[used - u - 1] = id;
-      p.remap[id] = id;
-      p.refs_out[id] = ref[i];
+      if (ref[i] > 0 && id >= used) {
+        p.from[used - u - 1] = id;
+        p.number[id] = used - u - 1;
+      }
       u += ref[i] > 0;
     }
-    // the holes below `used` are those before it less the used pages before it
-    if (b0 <= used && used < b0 + 4 * kPlanThreads) {
-      const int t = (int)((used - b0) / 4);
-      if (tid == t) {
-        int below = u;  // used pages below b + 4; take back those at or past `used`
-#pragma unroll
-        for (int i = 0; i < 4; ++i) below -= b + i >= used && ref[i] > 0;
-        *p.moves = used - below;
-      }
-    }
-    before += total;
-  }
-  if (used == blocks && tid == 0) *p.moves = 0;
-  __syncthreads();
-  const int moves = __ldcg(p.moves);
-  for (int i = tid; i < moves; i += kPlanThreads) {
-    const int a = __ldcg(p.from + i), b = __ldcg(p.to + i);
-    p.remap[a] = b;
-    p.refs_out[b] = __ldcg(p.refs + a);
-    p.refs_out[a] = 0;
   }
 }
 
 __global__ void __launch_bounds__(kCompactThreads) compact_apply_kernel(
     const __grid_constant__ CacheCompactParams p) {
-  const int moves = __ldg(p.moves);
+  grid_wait_prerequisite();
+  const int moves = __ldcg(p.head), used = __ldcg(p.head + 1);
   const int page = p.c.num_kv_heads * p.c.head_size * 2;  // 16-byte pieces
   const int groups = (page + kPieceGroup - 1) / kPieceGroup;
   const long long tasks = (long long)moves * groups * 2;
   for (long long x = blockIdx.x; x < tasks; x += gridDim.x) {
     const bool value = x & 1;
     const int g = (int)((x >> 1) % groups), i = (int)((x >> 1) / groups);
-    const size_t from = (size_t)__ldg(p.from + i) * page, to = (size_t)__ldg(p.to + i) * page;
+    const size_t from = (size_t)__ldcg(p.from + i) * page, to = (size_t)__ldcg(p.to + i) * page;
     uint4* c = static_cast<uint4*>(value ? p.c.v_cache : p.c.k_cache);
     copy_pieces<kCompactThreads>(c + from, c + to, g * kPieceGroup,
                                  min(page, (g + 1) * kPieceGroup));
   }
+  const long long first = (long long)blockIdx.x * kCompactThreads + threadIdx.x;
+  const long long step = (long long)gridDim.x * kCompactThreads;
+  // counts: every page is one move's source or target, or keeps its own.  (In
+  // place the last is nothing to do, so nothing else reads what a move writes.)
+  for (long long i = first; i < moves; i += step) {
+    const int from = __ldcg(p.from + i), to = __ldcg(p.to + i);
+    p.refs_out[to] = p.refs[from];
+    p.refs_out[from] = 0;
+  }
+  if (p.refs_out != p.refs)
+    for (long long b = first; b < p.c.num_blocks; b += step) {
+      const int ref = p.refs[b];
+      if ((ref > 0) == (b < used)) p.refs_out[b] = ref;
+    }
   const long long entries = (long long)p.c.num_seqs * p.c.max_blocks;
-  for (long long e = (long long)blockIdx.x * kCompactThreads + threadIdx.x; e < entries;
-       e += (long long)gridDim.x * kCompactThreads) {
+  for (long long e = first; e < entries; e += step) {
     const int row = (int)(e / p.c.max_blocks), col = (int)(e - (long long)row * p.c.max_blocks);
     int id = p.block_tables[e];
     if ((long long)col * kPage < __ldg(p.seq_lens + row)) {
-      if (id < 0 || id >= p.c.num_blocks)
+      if (id < 0 || id >= p.c.num_blocks) {
         atomicOr(p.c.status, kPageStatusBadBlock);
-      else
-        id = __ldg(p.remap + id);
+      } else if (id >= used) {
+        const int i = __ldcg(p.number + id);
+        if (i >= 0 && i < moves && __ldcg(p.from + i) == id) id = __ldcg(p.to + i);
+      }
     }
     p.block_tables_out[e] = id;
   }
+}
+
+// Launches a kernel that may start while the one before it on the stream still
+// runs (it waits for that one's end before it reads anything).
+template <class Params>
+cudaError_t launch_behind(void (*kernel)(Params), dim3 grid, int threads, const Params& p,
+                          cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace
@@ -526,11 +583,11 @@ __global__ void __launch_bounds__(kCompactThreads) compact_apply_kernel(
 cudaError_t launch_cache_write(const CacheWriteParams& p, cudaStream_t stream) {
   // a page's heads in groups that give each thread one value item
   const int pieces = p.c.head_size / 8;
-  const int group = std::min(p.c.num_kv_heads, std::max(1, kWriteThreads / (2 * pieces)));
+  const int group = std::min(p.c.num_kv_heads, kWriteThreads / (2 * pieces));
   const long long groups = (p.c.num_kv_heads + group - 1) / group;
   // n tokens touch at most n / 16 + 2 pages
-  const long long most = ((long long)p.total_tokens / kPage + 2LL * p.c.num_seqs) * groups;
-  const int grid = (int)std::min<long long>(most, (long long)p.c.sm_count * 8);
+  const long long most = (p.total_tokens / kPage + 2LL * p.c.num_seqs) * groups;
+  const int grid = (int)std::min<long long>(most, p.c.sm_count * 4LL);
   cache_write_kernel<<<grid, kWriteThreads, 0, stream>>>(p, group);
   return cudaGetLastError();
 }
@@ -552,16 +609,14 @@ cudaError_t launch_cache_fork(const CacheForkParams& p, cudaStream_t stream) {
   fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fork_apply_kernel<<<dim3(p.num_forks, kForkParts), kForkThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_behind(fork_apply_kernel, dim3(p.num_forks, kForkParts), kForkThreads, p, stream);
 }
 
 cudaError_t launch_cache_compact(const CacheCompactParams& p, cudaStream_t stream) {
   compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  compact_apply_kernel<<<p.c.sm_count * 4, kCompactThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_behind(compact_apply_kernel, dim3(p.c.sm_count * 4), kCompactThreads, p, stream);
 }
 
 }  // namespace avp

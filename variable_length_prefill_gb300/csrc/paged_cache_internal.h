@@ -79,7 +79,8 @@ struct CacheForkParams {
   int32_t* pages;
 };
 
-// Workspace of a compaction: moves[1], then remap, from and to [num_blocks].
+// Workspace of a compaction, all int32: head (moves, used pages), then for every
+// page the number of its move, and the moves' sources and targets.
 struct CacheCompactParams {
   CacheShape c;
   const int32_t* block_tables;
@@ -87,8 +88,8 @@ struct CacheCompactParams {
   const int32_t* refs;
   int32_t* block_tables_out;
   int32_t* refs_out;
-  int32_t* moves;
-  int32_t* remap;
+  int32_t* head;
+  int32_t* number;
   int32_t* from;
   int32_t* to;
 };

@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       float* part = reinterpret_cast<float*>(p.workspace + tree_parts_offset()) +
                     (size_t)(2 * blockIdx.x + (x.t0 == 0)) * tree_part_floats(D) + r;
       T* dst = static_cast<T*>(p.out) + row_at(x, r);
-      if (ok && !whole && copy == 0 && grp == 0) {
+      if (ok && !whole && row < rows && grp == 0) {
         part[D * kTreeRows] = mm;
         part[(D + 1) * kTreeRows] = ll;
       }
@@ -988,10 +988,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           for (int i = 0; i < 8; ++i)
             if (!(sum[i] - sum[i] == 0.f)) o[i] = sum[i];
         }
+        if (r >= rows) return;
         if (!whole) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) part[(c + i) * kTreeRows] = o[i];
-        } else if (r < rows) {
+        } else {
           *reinterpret_cast<uint4*>(dst + c) = make_uint4(
               Half16<T>::pack(o[0] * scale, o[1] * scale), Half16<T>::pack(o[2] * scale, o[3] * scale),
               Half16<T>::pack(o[4] * scale, o[5] * scale), Half16<T>::pack(o[6] * scale, o[7] * scale));
@@ -1081,64 +1082,99 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
 }
 
 // Joins the partial results of the row tile that CTA blockIdx.x began and
-// others went on with: 32 rows a CTA (blockIdx.y), a row a lane, D / 8 columns
-// a warp, the parts in CTA order.
+// others went on with: 32 rows (blockIdx.y) and 64 columns (blockIdx.z) a CTA,
+// a row a lane, 8 columns a warp, the parts in CTA order.  A few dozen parts
+// are read one behind the other, so what counts is loads in flight: the parts'
+// factors are found first, by all warps, and then kJoinParts parts are read at
+// a time (one by one, a tile of 30 parts took 60 us).
 constexpr int kJoinThreads = 256;
+constexpr int kJoinCols = 64;
+constexpr int kJoinParts = 4;
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeParams p) {
-  constexpr int COLS = D / 8;
+  __shared__ float s_m[kJoinThreads / 32][32], s_l[kJoinThreads / 32][32];
+  __shared__ float s_f[kTreeMaxCtas][32];
+  constexpr int WARPS = kJoinThreads / 32;
   grid_wait_prerequisite();
   const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const TreeOpen open = reinterpret_cast<const TreeOpen*>(p.workspace)[cta];
   const int group = p.num_query_heads / p.c.num_kv_heads;
   const int r0 = open.mt * kTreeRows, row = 32 * blockIdx.y + lane;
-  if (!open.valid || open.n * group - r0 <= 32 * (int)blockIdx.y) return;
+  const int rows = open.valid ? min(kTreeRows, open.n * group - r0) : 0;
+  if (32 * (int)blockIdx.y >= rows) return;
+  const bool live = row < rows;  // rows past the last have no partial results
   const float* parts = reinterpret_cast<const float*>(p.workspace + tree_parts_offset());
   auto part = [&](int k) {
     return parts + (size_t)(k == cta ? 2 * cta + 1 : 2 * k) * tree_part_floats(D) + row;
   };
+  // the row's maximum, and the parts' factors and sums
   float mm = -INFINITY;
-  bool nan = false, weightless = false;
-  for (int k = cta; k <= open.last; ++k) {
-    const float* a = part(k);
-    const float m = a[D * kTreeRows], l = a[(D + 1) * kTreeRows];
+  for (int k = cta + warp; k <= open.last; k += WARPS) {
+    const float m = live ? part(k)[D * kTreeRows] : -INFINITY;
+    s_f[k - cta][lane] = m;
     mm = fmaxf(mm, m);
+  }
+  s_m[warp][lane] = mm;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, s_m[w][lane]);
+  float ll = 0.f;
+  bool nan = false, weightless = false;
+  for (int k = cta + warp; k <= open.last; k += WARPS) {
+    const float m = s_f[k - cta][lane], l = live ? part(k)[(D + 1) * kTreeRows] : 0.f;
+    const float f = m == -INFINITY ? 0.f : ex2(m - mm);
+    if (f > 0.f) ll += f * l;
     nan |= !(l == l);
     weightless |= l == -1.f;
+    s_f[k - cta][lane] = f;
   }
-  float o[COLS], ll = 0.f;
+  __syncthreads();  // s_m is read
+  s_m[warp][lane] = ll;
+  s_l[warp][lane] = nan ? 2.f : (weightless ? 1.f : 0.f);
+  __syncthreads();
+  ll = 0.f;
+  float state = 0.f;
 #pragma unroll
-  for (int i = 0; i < COLS; ++i) o[i] = 0.f;
-  for (int k = cta; k <= open.last; ++k) {
-    const float* a = part(k);
-    const float m = a[D * kTreeRows];
-    const float f = m == -INFINITY ? 0.f : ex2(m - mm);
-    if (f > 0.f) ll += f * a[(D + 1) * kTreeRows];
-#pragma unroll
-    for (int i = 0; i < COLS; ++i) {
-      const float e = a[(warp * COLS + i) * kTreeRows];
-      // part of a row without weight: nothing but non-finite values of drafts
-      o[i] += f != 0.f ? f * e : (e - e == 0.f ? 0.f : e);
-    }
+  for (int w = 0; w < WARPS; ++w) {
+    ll += s_m[w][lane];
+    state = fmaxf(state, s_l[w][lane]);
   }
   float scale = 1.f / ll;
-  if (nan || (mm == -INFINITY && weightless)) scale = __uint_as_float(0x7fc00000u);
+  if (state == 2.f || (mm == -INFINITY && state == 1.f)) scale = __uint_as_float(0x7fc00000u);
   else if (mm == -INFINITY) scale = 0.f;
-  if (r0 + row >= open.n * group) return;
+  if (!live) return;
+  const int c = blockIdx.z * kJoinCols + warp * 8;
+  float o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  auto add = [&](float f, const float (&e)[8]) {
+    // a factor of 0 does not silence a value that is not finite
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] += f != 0.f ? f * e[i] : (e[i] - e[i] == 0.f ? 0.f : e[i]);
+  };
+  int k = cta;
+  for (; k + kJoinParts - 1 <= open.last; k += kJoinParts) {
+    float e[kJoinParts][8];
+#pragma unroll
+    for (int x = 0; x < kJoinParts; ++x)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[x][i] = part(k + x)[(c + i) * kTreeRows];
+#pragma unroll
+    for (int x = 0; x < kJoinParts; ++x) add(s_f[k + x - cta][lane], e[x]);
+  }
+  for (; k <= open.last; ++k) {
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = part(k)[(c + i) * kTreeRows];
+    add(s_f[k - cta][lane], e);
+  }
   const int j = (r0 + row) / group;
   T* dst = static_cast<T*>(p.out) +
-           ((size_t)(open.lo + j) * p.num_query_heads + open.g * group + (r0 + row - j * group)) * D +
-           warp * COLS;
-#pragma unroll
-  for (int i = 0; i < COLS; i += 8) {
-    uint4 w;
-    w.x = Half16<T>::pack(o[i] * scale, o[i + 1] * scale);
-    w.y = Half16<T>::pack(o[i + 2] * scale, o[i + 3] * scale);
-    w.z = Half16<T>::pack(o[i + 4] * scale, o[i + 5] * scale);
-    w.w = Half16<T>::pack(o[i + 6] * scale, o[i + 7] * scale);
-    *reinterpret_cast<uint4*>(dst + i) = w;
-  }
+           ((size_t)(open.lo + j) * p.num_query_heads + open.g * group + (r0 + row - j * group)) * D + c;
+  *reinterpret_cast<uint4*>(dst) = make_uint4(
+      Half16<T>::pack(o[0] * scale, o[1] * scale), Half16<T>::pack(o[2] * scale, o[3] * scale),
+      Half16<T>::pack(o[4] * scale, o[5] * scale), Half16<T>::pack(o[6] * scale, o[7] * scale));
 }
 
 template <int D, typename T>
@@ -1158,7 +1194,7 @@ cudaError_t launch_dt(const TreeParams& p, cudaStream_t stream) {
   tree_kernel<D, T><<<grid, C::THREADS, C::BYTES, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, kTreeRows / 32);
+  cfg.gridDim = dim3(grid, kTreeRows / 32, D / kJoinCols);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
