@@ -75,9 +75,6 @@ constexpr int kAncStride = kAncWords + 1;  // words between rows of the ancestor
 constexpr int kMaskDepth = 8;              // key tiles whose page masks are kept
 constexpr int kSegDepth = 4;               // published segments
 constexpr int kStageCols = 32;             // columns of an output step
-// A row tile's fixed cost (query rows in, filling the pipeline, output) in key
-// tiles, for the CTAs' equal shares.
-constexpr int kTileOverhead = 3;
 
 // A CTA's part of one row tile: key tiles [t0, t1) of nt.
 struct Segment {
@@ -102,6 +99,9 @@ struct TreeCfg {
   static constexpr uint32_t UNIT = BLK * PAGE;           // a key or value tile
   static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? 5 : 6);
   static constexpr int SOFTMAX = 128 * NG;  // softmax threads
+  // A row tile's fixed cost (query rows in, filling the pipeline, output) in key
+  // tiles, for the CTAs' equal shares.
+  static constexpr int OVERHEAD = D == 256 ? 10 : 6;
   static constexpr int THREADS = SOFTMAX + 128;
   // Warps past the softmax groups
   static constexpr int FIX = 4 * NG, PROD = 4 * NG + 2, MMA = 4 * NG + 3;
@@ -212,7 +212,7 @@ struct Walker {
         s = seq_info<D>(p, group, seq);
         known = seq;
       }
-      const int per = s.nt + kTileOverhead;  // units of a row tile: the overhead, then its tiles
+      const int per = s.nt + TreeCfg<D>::OVERHEAD;  // units of a row tile: the overhead, then its tiles
       if (off >= (long long)s.mts * p.c.num_kv_heads * per) {
         ++seq;
         off = 0;
@@ -220,8 +220,8 @@ struct Walker {
       }
       const long long tile = off / per;
       const int from = (int)(off - tile * per), take = (int)min((long long)per - from, end - u);
-      x.t0 = max(0, from - kTileOverhead);
-      x.t1 = from + take - kTileOverhead;
+      x.t0 = max(0, from - TreeCfg<D>::OVERHEAD);
+      x.t1 = from + take - TreeCfg<D>::OVERHEAD;
       x.u = u - from;
       u += take;
       off += take;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   const UnitRange range = locate_units<C::THREADS>(
       p.c.num_seqs, blockIdx.x, gridDim.x, scratch, [&](int i) -> long long {
         const SeqInfo s = seq_info<D>(p, group, i);
-        return (long long)s.mts * p.c.num_kv_heads * (s.nt + kTileOverhead);
+        return (long long)s.mts * p.c.num_kv_heads * (s.nt + TreeCfg<D>::OVERHEAD);
       });
   tc_fence_before();
   __syncthreads();
@@ -601,29 +601,42 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           __syncwarp();
           uint32_t odd = 0;
 #pragma unroll 1
-          for (int i = lane; i < ROWS; i += 32) {
-            const int d = i % D, q0 = p0 + (f * ROWS + i) / D * kPageTokens;
+          for (int pg = 0; pg < BLK / 2; ++pg) {
+            const int q0 = p0 + (f * (BLK / 2) + pg) * kPageTokens;
             if (q0 + kPageTokens <= edge || q0 >= x.len) continue;
+            // the words of a row: tokens past the last, and drafts (sign bits)
+            uint32_t past[8], draft[8];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint4* piece = reinterpret_cast<uint4*>(v + i * 32 + ((half ^ (d >> 2 & 1)) * 16));
-              uint4 e = *piece;
-              uint32_t* w = reinterpret_cast<uint32_t*>(&e);
-              uint32_t change = 0;
+            for (int k = 0; k < 8; ++k) {
+              const int pos = q0 + 2 * k;
+              past[k] = (pos >= x.len ? 0xffffu : 0u) | (pos + 1 >= x.len ? 0xffff0000u : 0u);
+              draft[k] = ((pos >= x.base ? 0x8000u : 0u) | (pos + 1 >= x.base ? 0x80000000u : 0u)) &
+                         ~past[k];
+            }
+#pragma unroll 2
+            for (int d = lane; d < D; d += 32) {
+              uint8_t* at = v + (pg * D + d) * 32;
+              uint4* piece[2] = {reinterpret_cast<uint4*>(at + (d >> 2 & 1) * 16),
+                                 reinterpret_cast<uint4*>(at + ((d >> 2 & 1) ^ 1) * 16)};
+              const uint4 e[2] = {*piece[0], *piece[1]};
+              uint32_t w[8] = {e[0].x, e[0].y, e[0].z, e[0].w, e[1].x, e[1].y, e[1].z, e[1].w};
+              // adding the distance from the least non-finite magnitude to the
+              // sign bit sets that bit for those that reach it, in both halves
+              constexpr uint32_t kToSign = (0x8000u - Half16<T>::kExp) * 0x10001u;
+              uint32_t wild[8], any = 0;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int pos = q0 + half * 8 + 2 * k;
-                const uint32_t past = (pos >= x.len ? 0xffffu : 0u) |
-                                      (pos + 1 >= x.len ? 0xffff0000u : 0u);
-                const uint32_t draft = (pos >= x.base ? 0xffffu : 0u) |
-                                       (pos + 1 >= x.base ? 0xffff0000u : 0u);
-                constexpr uint32_t kExp2 = Half16<T>::kExp * 0x10001u;
-                const uint32_t wild = __vcmpeq2(w[k] & kExp2, kExp2) & draft & ~past;
-                odd |= wild;
-                change |= w[k] & (wild | past);
-                w[k] &= ~(wild | past);
+              for (int k = 0; k < 8; ++k) {
+                wild[k] = ((w[k] & 0x7fff7fffu) + kToSign) & draft[k];
+                any |= wild[k];
+                w[k] &= ~past[k];
               }
-              if (change) *piece = e;
+              if (any) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] &= ~((wild[k] >> 15) * 0xffffu);
+              }
+              odd |= any;
+              *piece[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              *piece[1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
           }
           if (odd) s_odd[2 * a2 + f] = 1;
@@ -953,50 +966,33 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         part[D * kTreeRows] = mm;
         part[(D + 1) * kTreeRows] = ll;
       }
-      // eight columns of a row: to the output or to the partial results
-      auto put = [&](int c, float (&o)[8]) {
-        // The values of drafts were looked at; weights of 0 (a copy's for the
-        // keys of the others, a factor's) turn an infinity of the context into
-        // a NaN.  Where either shows, the sum of the non-finite values that the
-        // row sees in this segment is the result (a NaN of the scores is one
-        // anyway).
-        float wild = 0.f;
+      // The values of drafts were looked at; weights of 0 (a copy's for the keys
+      // of the others, a factor's) turn an infinity of the context into a NaN.
+      // Where either shows, the sum of the non-finite values that the row sees
+      // in this segment is the result (a NaN of the scores is one anyway).
+      auto mend = [&](int c, float (&o)[8]) {
+        float sum[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wild += o[i] - o[i];
-        if (r < rows && !nan && (odd || !(wild == 0.f))) {
-          float sum[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-          const int to = (int)min((long long)x.len, (long long)x.t1 * NT);
+        for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+        const int to = (int)min((long long)x.len, (long long)x.t1 * NT);
 #pragma unroll 1
-          for (int pos = x.t0 * NT; pos < to; ++pos) {
-            const int a = pos - x.base;
-            if (a >= 0 && !(anc[a >> 5] >> (a & 31) & 1u)) continue;
-            const int id =
-                __ldg(p.block_tables + (size_t)x.seq * p.c.max_blocks + pos / kPageTokens);
-            if (id < 0 || id >= p.c.num_blocks) continue;
-            const uint16_t* v = static_cast<const uint16_t*>(p.c.v_cache) +
-                                (((size_t)id * p.c.num_kv_heads + x.g) * D + c) * kPageTokens +
-                                pos % kPageTokens;
+        for (int pos = x.t0 * NT; pos < to; ++pos) {
+          const int a = pos - x.base;
+          if (a >= 0 && !(anc[a >> 5] >> (a & 31) & 1u)) continue;
+          const int id = __ldg(p.block_tables + (size_t)x.seq * p.c.max_blocks + pos / kPageTokens);
+          if (id < 0 || id >= p.c.num_blocks) continue;
+          const uint16_t* v = static_cast<const uint16_t*>(p.c.v_cache) +
+                              (((size_t)id * p.c.num_kv_heads + x.g) * D + c) * kPageTokens +
+                              pos % kPageTokens;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint16_t e = v[i * kPageTokens];
-              if ((e & Half16<T>::kExp) == Half16<T>::kExp) sum[i] += Half16<T>::widen(e);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const uint16_t e = v[i * kPageTokens];
+            if ((e & Half16<T>::kExp) == Half16<T>::kExp) sum[i] += Half16<T>::widen(e);
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (!(sum[i] - sum[i] == 0.f)) o[i] = sum[i];
         }
-        if (r >= rows) return;
-        if (!whole) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) part[(c + i) * kTreeRows] = o[i];
-        } else {
-          *reinterpret_cast<uint4*>(dst + c) = make_uint4(
-              Half16<T>::pack(o[0] * scale, o[1] * scale), Half16<T>::pack(o[2] * scale, o[3] * scale),
-              Half16<T>::pack(o[4] * scale, o[5] * scale), Half16<T>::pack(o[6] * scale, o[7] * scale));
-        }
+        for (int i = 0; i < 8; ++i)
+          if (!(sum[i] - sum[i] == 0.f)) o[i] = sum[i];
       };
       tc_fence_after();
 #pragma unroll 1
@@ -1005,49 +1001,63 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < kStageCols; ++i) o[i] = 0.f;
         if (ok) {
+          uint32_t e[NG][kStageCols];
+          __syncwarp();
 #pragma unroll
-          for (int a = 0; a < NG; ++a) {
-            if (a >= nt) break;  // a group without tiles
-            uint32_t e[kStageCols];
-            __syncwarp();
-            tmem_ld32(tmem + lanes + C::O(a) + c, e);
-            tmem_wait_ld();
-            // an accumulator that saw no key of the row may hold anything
+          for (int a = 0; a < NG; ++a) tmem_ld32(tmem + lanes + C::O(a) + c, e[a]);
+          tmem_wait_ld();
+          // an accumulator that saw no key of the row may hold anything
+#pragma unroll
+          for (int a = 0; a < NG; ++a)
 #pragma unroll
             for (int i = 0; i < kStageCols; ++i)
-              o[i] = f[a] < 0.f ? o[i] : fmaf(f[a], __uint_as_float(e[i]), o[i]);
-          }
+              o[i] = f[a] < 0.f ? o[i] : fmaf(f[a], __uint_as_float(e[a][i]), o[i]);
         }
-        if (copies == 1) {
-          if (ok) {
-#pragma unroll
-            for (int i = 0; i < kStageCols; i += 8) {
-              float w[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = o[i + k];
-              put(c + i, w);
-            }
-          }
-        } else {
-          // the copies of a row meet in shared memory; each puts its share of
-          // the columns
+        // The copies of a row meet in shared memory, and each goes on with its
+        // share of the columns: o[0 .. width).
+        int c0 = c, width = kStageCols;
+        if (copies > 1) {
 #pragma unroll
           for (int i = 0; i < kStageCols; ++i) stage[i * kTreeRows + row] = o[i];
           softmax_barrier(2 + grp, 128);
-          if (ok) {
-#pragma unroll 1
-            for (int i = copy * (kStageCols / copies); i < (copy + 1) * (kStageCols / copies); i += 8) {
-              float w[8];
+          width = kStageCols / copies;
+          c0 += copy * width;
+          const float* at = stage + copy * width * kTreeRows + r;
+          if (copies == 2) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float* at = stage + (i + k) * kTreeRows + r;
-                w[k] = at[0] + at[span];
-                if (copies == 4) w[k] += at[2 * span] + at[3 * span];
-              }
-              put(c + i, w);
-            }
+            for (int i = 0; i < kStageCols / 2; ++i)
+              o[i] = at[i * kTreeRows] + at[i * kTreeRows + kTreeRows / 2];
+          } else {
+#pragma unroll
+            for (int i = 0; i < kStageCols / 4; ++i)
+              o[i] = (at[i * kTreeRows] + at[i * kTreeRows + kTreeRows / 4]) +
+                     (at[i * kTreeRows + kTreeRows / 2] + at[i * kTreeRows + kTreeRows / 4 * 3]);
           }
           softmax_barrier(2 + grp, 128);
+        }
+        if (r >= rows || !ok) continue;
+        float wild[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kStageCols; ++i)
+          if (i < width) wild[i % 4] += o[i] - o[i];
+        if (!nan && (odd || !((wild[0] + wild[1]) + (wild[2] + wild[3]) == 0.f))) {
+#pragma unroll
+          for (int i = 0; i < kStageCols; i += 8)
+            if (i < width) mend(c0 + i, *reinterpret_cast<float(*)[8]>(o + i));
+        }
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < kStageCols; ++i)
+            if (i < width) part[(c0 + i) * kTreeRows] = o[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < kStageCols; i += 8)
+            if (i < width)
+              *reinterpret_cast<uint4*>(dst + c0 + i) =
+                  make_uint4(Half16<T>::pack(o[i] * scale, o[i + 1] * scale),
+                             Half16<T>::pack(o[i + 2] * scale, o[i + 3] * scale),
+                             Half16<T>::pack(o[i + 4] * scale, o[i + 5] * scale),
+                             Half16<T>::pack(o[i + 6] * scale, o[i + 7] * scale));
         }
       }
       __syncwarp();
@@ -1058,7 +1068,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       }
       if (!whole && x.t0 == 0) {
         const long long used = range.total < gridDim.x ? range.total : gridDim.x;
-        const long long next = x.u + x.nt + kTileOverhead;  // the unit behind the row tile
+        const long long next = x.u + x.nt + TreeCfg<D>::OVERHEAD;  // the unit behind the row tile
         open = {1, x.lo, x.n, x.g, x.mt,
                 (int)((next * used + range.total - 1) / range.total) - 1, {0, 0}};
       }
@@ -1085,7 +1095,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
 // others went on with: 32 rows (blockIdx.y) and 64 columns (blockIdx.z) a CTA,
 // a row a lane, 8 columns a warp, the parts in CTA order.  A few dozen parts
 // are read one behind the other, so what counts is loads in flight: the parts'
-// factors are found first, by all warps, and then kJoinParts parts are read at
+// factors are found first, by all warps, and kJoinParts parts are read at
 // a time (one by one, a tile of 30 parts took 60 us).
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCols = 64;
@@ -1108,11 +1118,22 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   auto part = [&](int k) {
     return parts + (size_t)(k == cta ? 2 * cta + 1 : 2 * k) * tree_part_floats(D) + row;
   };
+  const int c = blockIdx.z * kJoinCols + warp * 8, count = open.last - cta + 1;
+  float e[kJoinParts][8];
+  auto read = [&](int k0) {
+#pragma unroll
+    for (int x = 0; x < kJoinParts; ++x)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        e[x][i] = live && k0 + x < count ? part(cta + k0 + x)[(c + i) * kTreeRows] : 0.f;
+  };
+  read(0);
   // the row's maximum, and the parts' factors and sums
-  float mm = -INFINITY;
-  for (int k = cta + warp; k <= open.last; k += WARPS) {
-    const float m = live ? part(k)[D * kTreeRows] : -INFINITY;
-    s_f[k - cta][lane] = m;
+  float mm = -INFINITY, l0 = 0.f;  // l0: the sum of this warp's first part
+  for (int k = warp; k < count; k += WARPS) {
+    const float m = live ? part(cta + k)[D * kTreeRows] : -INFINITY;
+    if (k == warp) l0 = live ? part(cta + k)[(D + 1) * kTreeRows] : 0.f;
+    s_f[k][lane] = m;
     mm = fmaxf(mm, m);
   }
   s_m[warp][lane] = mm;
@@ -1121,13 +1142,14 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, s_m[w][lane]);
   float ll = 0.f;
   bool nan = false, weightless = false;
-  for (int k = cta + warp; k <= open.last; k += WARPS) {
-    const float m = s_f[k - cta][lane], l = live ? part(k)[(D + 1) * kTreeRows] : 0.f;
+  for (int k = warp; k < count; k += WARPS) {
+    const float m = s_f[k][lane];
+    const float l = k == warp ? l0 : (live ? part(cta + k)[(D + 1) * kTreeRows] : 0.f);
     const float f = m == -INFINITY ? 0.f : ex2(m - mm);
     if (f > 0.f) ll += f * l;
     nan |= !(l == l);
     weightless |= l == -1.f;
-    s_f[k - cta][lane] = f;
+    s_f[k][lane] = f;
   }
   __syncthreads();  // s_m is read
   s_m[warp][lane] = ll;
@@ -1143,32 +1165,22 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   float scale = 1.f / ll;
   if (state == 2.f || (mm == -INFINITY && state == 1.f)) scale = __uint_as_float(0x7fc00000u);
   else if (mm == -INFINITY) scale = 0.f;
-  if (!live) return;
-  const int c = blockIdx.z * kJoinCols + warp * 8;
   float o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  auto add = [&](float f, const float (&e)[8]) {
-    // a factor of 0 does not silence a value that is not finite
+  for (int k = 0; k < count; k += kJoinParts) {
+    if (k) read(k);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] += f != 0.f ? f * e[i] : (e[i] - e[i] == 0.f ? 0.f : e[i]);
-  };
-  int k = cta;
-  for (; k + kJoinParts - 1 <= open.last; k += kJoinParts) {
-    float e[kJoinParts][8];
+    for (int x = 0; x < kJoinParts; ++x) {
+      if (k + x >= count) break;
+      const float f = s_f[k + x][lane];
+      // a factor of 0 does not silence a value that is not finite
 #pragma unroll
-    for (int x = 0; x < kJoinParts; ++x)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[x][i] = part(k + x)[(c + i) * kTreeRows];
-#pragma unroll
-    for (int x = 0; x < kJoinParts; ++x) add(s_f[k + x - cta][lane], e[x]);
+      for (int i = 0; i < 8; ++i)
+        o[i] += f != 0.f ? f * e[x][i] : (e[x][i] - e[x][i] == 0.f ? 0.f : e[x][i]);
+    }
   }
-  for (; k <= open.last; ++k) {
-    float e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = part(k)[(c + i) * kTreeRows];
-    add(s_f[k - cta][lane], e);
-  }
+  if (!live) return;
   const int j = (r0 + row) / group;
   T* dst = static_cast<T*>(p.out) +
            ((size_t)(open.lo + j) * p.num_query_heads + open.g * group + (r0 + row - j * group)) * D + c;
