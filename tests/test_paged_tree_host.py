@@ -22,6 +22,8 @@ BIG = 1 << 40
     ((P,) * 7 + (1, 4, 8, 2, 128, 32, 1, 1, 0.0, 0, P, P, BIG, None), B.ERR_INVALID_ARG),
     ((P,) * 7 + (1, 4, 8, 2, 128, 16, 1, 1, 0.0, 2, P, P, BIG, None), B.ERR_INVALID_ARG),
     ((P,) * 7 + (1, 4, 8, 2, 128, 16, 1, 1, float("nan"), 0, P, P, BIG, None), B.ERR_INVALID_ARG),
+    ((P,) * 7 + (1, 1 << 30, 8, 2, 128, 16, 1, 1, 0.0, 0, P, P, BIG, None), B.ERR_INVALID_ARG),
+    ((P,) * 7 + (1, 4, 8, 2, 128, 16, 1 << 27, 1, 0.0, 0, P, P, BIG, None), B.ERR_INVALID_ARG),
     ((P,) * 7 + (1, 4, 8, 2, 128, 16, 1, 1, float("inf"), 0, P, P, BIG, None), B.ERR_INVALID_ARG),
     ((P,) * 7 + (1, 4, 8, 2, 128, 16, 1, 1, 0.0, 0, None, P, BIG, None), B.ERR_INVALID_ARG),
     ((P,) * 7 + (1, 4, 8, 2, 128, 16, 1, 1, 0.0, 0, P, None, BIG, None), B.ERR_INVALID_ARG),

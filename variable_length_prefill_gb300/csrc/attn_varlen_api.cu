@@ -739,7 +739,10 @@ int paged_attn_tree(const void* query, const void* k_cache, const void* v_cache,
                        num_blocks);
   if (!rc) rc = check_arrays({block_tables, seq_lens, cu_seqlens, query, out, workspace});
   if (rc) return rc;
-  if ((int64_t)num_query_heads * head_size > (1 << 22)) return ATTN_VARLEN_ERR_INVALID_ARG;
+  // rows and positions are counted in 32 bits
+  if ((int64_t)num_query_heads * head_size > (1 << 22) || max_blocks_per_seq > (1 << 26) ||
+      (int64_t)total_q * (num_query_heads / num_kv_heads) > (1 << 30))
+    return ATTN_VARLEN_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(query) | reinterpret_cast<uintptr_t>(out) |
        reinterpret_cast<uintptr_t>(workspace)) & 15u)
     return ATTN_VARLEN_ERR_MISALIGNED;
@@ -762,6 +765,7 @@ int paged_attn_tree(const void* query, const void* k_cache, const void* v_cache,
   p.num_query_heads = num_query_heads;
   const double s = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)head_size);
   p.scale_log2 = (float)(1.4426950408889634 * s);
+  p.test_withhold = g_test_withhold;
   return map_cuda(avp::launch_tree(p, dtype == PAGED_ATTN_FP16, stream));
 }
 

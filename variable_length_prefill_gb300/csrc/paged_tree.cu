@@ -399,6 +399,12 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       auto issue = [&](int t, bool value) -> bool {
         const uint32_t u = issued, s = u % C::STAGES;
         if (!wait(C::EMPTY + s, ((u / C::STAGES) & 1u) ^ 1u)) return false;
+#if ATTN_VARLEN_TEST_HOOKS
+        if (p.test_withhold && x.u == 0 && x.t0 == 0 && u == 0) {  // not copied, not announced
+          ++issued;
+          return true;
+        }
+#endif
         const int page = t & 1 ? id[1] : id[0];
         const bool there = lane < BLK && page >= 0 && page < p.c.num_blocks;
         const uint32_t mask = __ballot_sync(0xffffffffu, there);

@@ -27,6 +27,7 @@ struct TreeParams {
   int total_q;
   int num_query_heads;
   float scale_log2;  // scale * log2(e)
+  int test_withhold; // read only by test builds (ATTN_VARLEN_TEST_HOOKS); 0 otherwise
 };
 
 // Workspace: kTreeMaxCtas TreeOpen records, then fp32 partial results
