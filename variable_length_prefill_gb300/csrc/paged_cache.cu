@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kWriteThreads, 4) cache_write_kernel(
   __shared__ UnitScratch scratch;
   const int groups = (p.c.num_kv_heads + head_group - 1) / head_group;
   const UnitRange range = locate_units<kWriteThreads>(
-      p.c.num_seqs, blockIdx.x, gridDim.x, scratch, [&](int i) -> long long {
+      p.c.num_seqs, blockIdx.x, gridDim.x, 1, scratch, [&](int i) -> long long {
         const NewTokens t = new_tokens(p.cu, p.seq_lens, i, p.total_tokens);
         return (long long)write_pages(t, p.c.max_blocks).pages * groups;
       });

@@ -100,9 +100,14 @@ struct TreeCfg {
   static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? 5 : 6);
   static constexpr int SOFTMAX = 128 * NG;  // softmax threads
   // A row tile's fixed cost (query rows in, filling the pipeline, output) in key
-  // tiles, for the CTAs' equal shares.
+  // tiles, for the CTAs' equal shares.  Counted as 3 / 6 / 10 / 15 tiles, 16
+  // sequences of up to 2112 tokens and 64 drafts at D = 256 took 66 / 55 / 51 /
+  // 52 us, and 64 x 4096 tokens at D = 128 186 / 185 / 187 / 189.
   static constexpr int OVERHEAD = D == 256 ? 10 : 6;
-  static constexpr int THREADS = SOFTMAX + 128;
+  // No share is smaller: below that, one more CTA on a row tile saves less than
+  // its partial results cost to join (5 sequences of up to 3239 tokens and one
+  // KV head: 28 us without a least share, 20 us with 4, 23 with 8, 27 with 12).
+  static constexpr int LEAST = OVERHEAD - 2;
   // Warps past the softmax groups
   static constexpr int FIX = 4 * NG, PROD = 4 * NG + 2, MMA = 4 * NG + 3;
   // the page masks of tile t are overwritten by tile t + kMaskDepth, whose
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   }
   const int group = p.num_query_heads / p.c.num_kv_heads;
   const UnitRange range = locate_units<C::THREADS>(
-      p.c.num_seqs, blockIdx.x, gridDim.x, scratch, [&](int i) -> long long {
+      p.c.num_seqs, blockIdx.x, gridDim.x, C::LEAST, scratch, [&](int i) -> long long {
         const SeqInfo s = seq_info<D>(p, group, i);
         return (long long)s.mts * p.c.num_kv_heads * (s.nt + TreeCfg<D>::OVERHEAD);
       });
@@ -1073,10 +1078,9 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         ++uses;
       }
       if (!whole && x.t0 == 0) {
-        const long long used = range.total < gridDim.x ? range.total : gridDim.x;
         const long long next = x.u + x.nt + TreeCfg<D>::OVERHEAD;  // the unit behind the row tile
         open = {1, x.lo, x.n, x.g, x.mt,
-                (int)((next * used + range.total - 1) / range.total) - 1, {0, 0}};
+                (int)((next * range.used + range.total - 1) / range.total) - 1, {0, 0}};
       }
       tiles += nt;
       ++count;

@@ -14,6 +14,7 @@ namespace {
 // `seq`.  Empty when u0 == u1.
 struct UnitRange {
   long long u0, u1, total;
+  int used;  // ranges that the units are cut into
   long long off;
   int seq;
 };
@@ -33,13 +34,14 @@ __device__ __forceinline__ long long warp_inclusive(long long x, int lane) {
   return x;
 }
 
-// Range `part` of `parts`; every thread of the CTA takes part.  count(i) is
-// the units of sequence i.  Thread t sums a run of consecutive sequences, a
+// Range `part` of at most `parts`, none shorter than `least` units unless there
+// are fewer; every thread of the CTA takes part.  count(i) is the units of
+// sequence i.  Thread t sums a run of consecutive sequences, a
 // scan over the threads gives the total, and the thread whose run holds unit
 // u0 walks it.
 template <int THREADS, class Count>
-__device__ __forceinline__ UnitRange locate_units(int n, int part, int parts, UnitScratch& s,
-                                                  Count count) {
+__device__ __forceinline__ UnitRange locate_units(int n, int part, int parts, int least,
+                                                  UnitScratch& s, Count count) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (n + THREADS - 1) / THREADS;
   const int a = min(n, tid * run), b = min(n, a + run);
@@ -58,9 +60,11 @@ __device__ __forceinline__ UnitRange locate_units(int n, int part, int parts, Un
     if (w < warp) before += s.warp_sum[w];
     total += s.warp_sum[w];
   }
-  const int used = (int)(total < parts ? total : parts);  // ranges that hold a unit
+  // ranges that hold units
+  const int used = (int)min((long long)parts, max(total / least, min(total, 1LL)));
   UnitRange r;
   r.total = total;
+  r.used = used;
   r.u0 = part < used ? total * part / used : total;
   r.u1 = part < used ? total * (part + 1) / used : total;
   if (r.u0 < r.u1 && before <= r.u0 && r.u0 < before + sum) {
