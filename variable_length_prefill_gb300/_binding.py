@@ -7,6 +7,7 @@ loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 
 from . import build as _build
@@ -342,6 +343,11 @@ def _elsewhere(dev, stream):
     return cuda.stream(stream)  # makes the stream's device current as well
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name, *sizes):
+    return getattr(load(), f"{name}_workspace_size")(*sizes)
+
+
 def _bytes(n, dev):
     return _torch_module.empty(n, dtype=_torch_module.uint8, device=dev)
 
@@ -462,7 +468,7 @@ def paged_attn_cache_fork(k_cache, v_cache, block_tables, seq_lens, refs, src, d
         with ctx:
             return paged_attn_cache_fork(k_cache, v_cache, block_tables, seq_lens, refs, src, dst)
     lib = _LIB or load()
-    size = lib.paged_attn_cache_fork_workspace_size(n, s)
+    size = _workspace_bytes("paged_attn_cache_fork", n, s)
     ws = _bytes(size, dev)
     _done(lib.paged_attn_cache_fork(
         k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
@@ -493,7 +499,7 @@ def paged_attn_cache_compact(k_cache, v_cache, block_tables, seq_lens, refs, out
         _ints(tables_out, (s, w), dev, "out block_tables")
         _ints(refs_out, (nb,), dev, "out refs")
     lib = _LIB or load()
-    size = lib.paged_attn_cache_compact_workspace_size(nb)
+    size = _workspace_bytes("paged_attn_cache_compact", nb)
     ws = _bytes(size, dev)
     _done(lib.paged_attn_cache_compact(
         k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
@@ -537,7 +543,7 @@ def paged_attn_tree(query, k_cache, v_cache, block_tables, seq_lens, cu_seqlens,
             return paged_attn_tree(query, k_cache, v_cache, block_tables, seq_lens, cu_seqlens,
                                    parents, scale or None, out)
     lib = _LIB or load()
-    size = lib.paged_attn_tree_workspace_size(d)
+    size = _workspace_bytes("paged_attn_tree", d)
     ws = _bytes(size, dev)
     if out is None:
         out = _torch_module.empty_like(query)

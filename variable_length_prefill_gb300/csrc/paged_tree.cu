@@ -108,6 +108,7 @@ struct TreeCfg {
   // its partial results cost to join (5 sequences of up to 3239 tokens and one
   // KV head: 28 us without a least share, 20 us with 4, 23 with 8, 27 with 12).
   static constexpr int LEAST = OVERHEAD - 2;
+  static constexpr int THREADS = SOFTMAX + 128;
   // Warps past the softmax groups
   static constexpr int FIX = 4 * NG, PROD = 4 * NG + 2, MMA = 4 * NG + 3;
   // the page masks of tile t are overwritten by tile t + kMaskDepth, whose
