@@ -161,8 +161,9 @@ int attn_varlen_fwd_ws(const void* q, const void* k, const void* v,
  * word of the current device's library-owned workspace.  Returns
  * ATTN_VARLEN_OK, ATTN_VARLEN_ERR_DEVICE_TIMEOUT when a kernel wait ran out of
  * time since the last check, or ATTN_VARLEN_ERR_CUDA when the stream reports
- * an error.  Also reads and clears the paged operators' status on the device
- * (ATTN_VARLEN_ERR_BAD_BLOCK_TABLE, _BAD_DRAFT, _NO_FREE_BLOCK, _BAD_ROW).
+ * an error.  Also reads and clears the paged operators' status on the device:
+ * of several reports it returns the first of ATTN_VARLEN_ERR_DEVICE_TIMEOUT,
+ * _BAD_BLOCK_TABLE, _NO_FREE_BLOCK, _BAD_DRAFT, _BAD_ROW.
  */
 int attn_varlen_check(cudaStream_t stream);
 

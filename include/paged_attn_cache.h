@@ -49,8 +49,8 @@ extern "C" {
  *   key, value   device [total_tokens, num_kv_heads, head_size]; the strides
  *                between tokens and between heads are given in elements, are
  *                >= 0 and multiples of 8; the head's elements are contiguous
- *   total_tokens packed rows; rows outside it are never read, rows that no
- *                sequence covers are not used
+ *   total_tokens packed rows; cu_seqlens is taken as clipped to
+ *                [0, total_tokens], rows that no sequence covers are not used
  *
  * A token whose position is negative is not written; nor is one at or past
  * max_blocks_per_seq * 16 (ATTN_VARLEN_ERR_BAD_BLOCK_TABLE).  Every other slot

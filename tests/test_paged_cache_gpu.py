@@ -82,6 +82,22 @@ def test_write(cuda_lib, rows, hkv, d, start, fused):
     np.testing.assert_array_equal(_bits(gv), v)
 
 
+def test_write_single_token_and_head_with_any_stride(cuda_lib):
+    """The stride of a dimension of one says nothing about the layout."""
+    rng = np.random.default_rng(14)
+    lens = np.asarray([21], dtype=np.int32)
+    tables, blocks = ref.tables_for(rng, lens)
+    k, v = ref.new_caches(rng, blocks, 1, 64)
+    x = rng.integers(0, 1 << 16, (1, 1, 64), dtype=np.uint16)
+    t = _bf16(x).as_strided((1, 1, 64), (3, 5, 1))
+    gk, gv = _bf16(k), _bf16(v)
+    cuda_lib.paged_attn_cache_write(t, t, gk, gv, _t(tables), _t(lens), _t(_cu([1])))
+    _raises(cuda_lib)
+    assert not ref.write(x, x, k, v, tables, lens, _cu([1]))
+    np.testing.assert_array_equal(_bits(gk), k)
+    np.testing.assert_array_equal(_bits(gv), v)
+
+
 def test_write_odd_calls(cuda_lib):
     """Slices that step backwards, lengths below the new tokens or negative,
     offsets past the packed rows: what has a place is written, no more."""

@@ -266,6 +266,12 @@ def test_scale(cuda_lib):
     Case([(70, 5)], 4, 2, 64, seed=13).check(cuda_lib, scale=0.37)
 
 
+@pytest.mark.parametrize("scale", [0.0, -1.0, 1e-46, 2.0 ** 127, float("inf"), float("nan")])
+def test_scales_that_32_bits_do_not_hold_are_refused(cuda_lib, scale):
+    with pytest.raises(ValueError, match="scale"):
+        Case([(7, 2)], 2, 1, 64, seed=15).check(cuda_lib, scale=scale)
+
+
 def test_lengths_below_the_drafts(cuda_lib):
     """Fewer tokens than drafts: those at negative positions do not exist, and
     a row that sees nothing is zero.  Negative lengths are empty."""

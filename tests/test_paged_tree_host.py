@@ -25,6 +25,7 @@ BIG = 1 << 40
     ((P,) * 7 + (1, 1 << 30, 8, 2, 128, 16, 1, 1, 0.0, 0, P, P, BIG, None), B.ERR_INVALID_ARG),
     ((P,) * 7 + (1, 4, 8, 2, 128, 16, 1 << 27, 1, 0.0, 0, P, P, BIG, None), B.ERR_INVALID_ARG),
     ((P,) * 7 + (1, 4, 8, 2, 128, 16, 1, 1, float("inf"), 0, P, P, BIG, None), B.ERR_INVALID_ARG),
+    ((P,) * 7 + (1, 4, 8, 2, 128, 16, 1, 1, 2.0 ** 127, 0, P, P, BIG, None), B.ERR_INVALID_ARG),
     ((P,) * 7 + (1, 4, 8, 2, 128, 16, 1, 1, 0.0, 0, None, P, BIG, None), B.ERR_INVALID_ARG),
     ((P,) * 7 + (1, 4, 8, 2, 128, 16, 1, 1, 0.0, 0, P, None, BIG, None), B.ERR_INVALID_ARG),
     ((None,) + (P,) * 6 + (1, 4, 8, 2, 128, 16, 1, 1, 0.0, 0, P, P, BIG, None), B.ERR_INVALID_ARG),

@@ -383,6 +383,10 @@ def paged_attn_cache_write(key, value, k_cache, v_cache, block_tables, seq_lens,
                                           cu_seqlens)
     kt, kh, _ = key.stride()
     vt, vh, _ = value.stride()
+    if total == 1:  # the stride of a single token or head says nothing
+        kt = vt = 0
+    if hkv == 1:
+        kh = vh = 0
     _done((_LIB or load()).paged_attn_cache_write(
         key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         block_tables.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), s, total, hkv, d, bs,
@@ -535,8 +539,8 @@ def paged_attn_tree(query, k_cache, v_cache, block_tables, seq_lens, cu_seqlens,
         _ints(parents, (total,), dev, "parents")
     if scale is None:
         scale = 0.0
-    elif not 0.0 < scale < float("inf"):
-        raise ValueError("scale must be positive and finite")
+    elif not 2.0 ** -126 <= scale <= 2.0 ** 126:  # the library takes it in 32 bits
+        raise ValueError("scale must be from 2^-126 to 2^126")
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:

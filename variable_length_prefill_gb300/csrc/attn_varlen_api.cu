@@ -747,7 +747,7 @@ int paged_attn_tree(const void* query, const void* k_cache, const void* v_cache,
        reinterpret_cast<uintptr_t>(workspace)) & 15u)
     return ATTN_VARLEN_ERR_MISALIGNED;
   if (reinterpret_cast<uintptr_t>(parents) & 3u) return ATTN_VARLEN_ERR_MISALIGNED;
-  if (!(scale == scale) || scale > 3.4e38f) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (!(scale == scale) || scale > 0x1p126f) return ATTN_VARLEN_ERR_INVALID_ARG;
   if (workspace_bytes < paged_attn_tree_workspace_size(head_size))
     return ATTN_VARLEN_ERR_WORKSPACE_SMALL;
   avp::TreeParams p;
