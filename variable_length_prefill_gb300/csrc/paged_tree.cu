@@ -123,8 +123,10 @@ struct TreeCfg {
   static constexpr bool Q_TMEM = D != 128;
   __host__ __device__ static constexpr uint32_t QT() { return (uint32_t)(2 * NT + NG * D); }
   static_assert(2 * NT + NG * D + (Q_TMEM ? D / 2 : 0) <= 512, "TMEM columns");
-  static constexpr int QN = D / 8 / NG;           // 16-byte pieces of a row per thread
-  static constexpr int QR = QN < 16 ? QN : 16;    // of them in registers at a time
+  // A group's part of a query row, in 16-byte pieces; a warp reads QP pieces of
+  // 32 / QP rows at a time
+  static constexpr int QN = D / 8 / NG;
+  static constexpr int QP = Q_TMEM && QN >= 8 ? 8 : 4;
   // shared memory, from a 1024-byte aligned base
   static constexpr uint32_t RING = 0;
   // query rows for D = 128, [D / 8][128 rows][16 bytes]; at the end of a segment
@@ -368,18 +370,16 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
                  ? __ldg(p.block_tables + (size_t)y.seq * p.c.max_blocks + i)
                  : -1;
     };
-    // a segment that will be published soon: its page ids, its query rows
-    auto ahead = [&](const Segment& y) {
-      ids = read_ids(y, 0);
-      next = read_ids(y, 1);
+    // a segment that is published soon: its query rows to L2
+    auto prefetch_query = [&](const Segment& y) {
       const int r0 = y.mt * kTreeRows;
       const int rows = (int)min((long long)kTreeRows, (long long)y.n * group - r0);
-      for (int i = lane; i < rows * (D / 64); i += 32) {
-        const int r = r0 + i / (D / 64), j = r / group;
+      for (int i = lane; i < rows; i += 32) {
+        const int j = (r0 + i) / group;
         const T* q = static_cast<const T*>(p.query) +
-                     ((size_t)(y.lo + j) * p.num_query_heads + y.g * group + (r - j * group)) * D +
-                     i % (D / 64) * 64;
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+                     ((size_t)(y.lo + j) * p.num_query_heads + y.g * group + (r0 + i - j * group)) * D;
+#pragma unroll
+        for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + d));
       }
       __syncwarp();
     };
@@ -395,8 +395,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       return true;
     };
     bool more = walk.next(p, group, x);
-    if (more) ahead(x);
     bool ok = publish(x);
+    if (more) {
+      ids = read_ids(x, 0);
+      next = read_ids(x, 1);
+    }
     while (ok && more) {
       const int nt = x.t1 - x.t0;
       const int pages = (x.len + kPageTokens - 1) / kPageTokens;
@@ -447,7 +450,10 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       for (int t = 0; ok && t < nt; ++t) {
         if (t == nt - 1) {
           more = walk.next(p, group, y);
-          if (more) ahead(y);
+          if (more) {
+            ids = read_ids(y, 0);
+            next = read_ids(y, 1);
+          }
         }
         ok = issue(t, true);
         if (ok && t + 2 < nt) ok = load_k(t + 2);
@@ -455,6 +461,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       if (!ok) break;
       tiles += nt;
       x = y;
+      if (more) prefetch_query(x);
       ok = publish(x);
     }
     // every copy has landed before the CTA can exit (also where others gave up)
@@ -550,48 +557,48 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       const int edge = min(x.base, x.len);
       const bool drafts = has_drafts();
       const uint32_t a2 = uses & 1u;
-      bool built = false;
+      if (drafts) {
+        // who sees whom: a bit per draft for every draft that has a row in the
+        // tile, by a walk up the tree (parents are below their children).  A
+        // few thousand clocks, so before the values, not when the drafts' tile
+        // needs it.
+        if (!(ok = wait(C::ANC_EMPTY + a2, ((uses >> 1) & 1u) ^ 1u))) break;
+        if (lane == 0) s_odd[2 * a2 + f] = 0;
+        for (int a = lane; a < x.n; a += 32) {
+          int up = p.parents ? __ldg(p.parents + x.lo + a) : a - 1;
+          if (up < -1 || up >= a) {
+            up = -1;
+            atomicOr(p.c.status, kPageStatusBadDraft);
+          }
+          s_parent[a] = up;
+        }
+        __syncwarp();
+        const int r0 = x.mt * kTreeRows, j0 = r0 / group;
+        const int last =
+            (int)min((long long)r0 + kTreeRows - 1, (long long)x.n * group - 1) / group;
+        uint32_t* table =
+            reinterpret_cast<uint32_t*>(bp + C::ANC) + a2 * kTreeRows * kAncStride;
+        for (int j = j0 + f * 32 + lane; j <= last; j += 64) {
+          uint32_t* mine = table + (j - j0) * kAncStride;
+#pragma unroll
+          for (int w = 0; w < kAncWords; ++w) mine[w] = 0;
+          uint32_t word = 0;
+          int at = j >> 5;
+          for (int a = j; a >= 0; a = s_parent[a]) {
+            if (a >> 5 != at) {
+              mine[at] = word;
+              word = 0;
+              at = a >> 5;
+            }
+            word |= 1u << (a & 31);
+          }
+          mine[at] = word;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::ANC_FULL + a2));
+      }
       for (int t = 0; t < nt; ++t) {
         const int p0 = (x.t0 + t) * NT;
-        if (drafts && !built && p0 + NT > edge) {
-          // who sees whom: a bit per draft for every draft that has a row in
-          // the tile, by a walk up the tree (parents are below their children)
-          if (!(ok = wait(C::ANC_EMPTY + a2, ((uses >> 1) & 1u) ^ 1u))) break;
-          if (lane == 0) s_odd[2 * a2 + f] = 0;
-          for (int a = lane; a < x.n; a += 32) {
-            int up = p.parents ? __ldg(p.parents + x.lo + a) : a - 1;
-            if (up < -1 || up >= a) {
-              up = -1;
-              atomicOr(p.c.status, kPageStatusBadDraft);
-            }
-            s_parent[a] = up;
-          }
-          __syncwarp();
-          const int r0 = x.mt * kTreeRows, j0 = r0 / group;
-          const int last =
-              (int)min((long long)r0 + kTreeRows - 1, (long long)x.n * group - 1) / group;
-          uint32_t* table =
-              reinterpret_cast<uint32_t*>(bp + C::ANC) + a2 * kTreeRows * kAncStride;
-          for (int j = j0 + f * 32 + lane; j <= last; j += 64) {
-            uint32_t* mine = table + (j - j0) * kAncStride;
-#pragma unroll
-            for (int w = 0; w < kAncWords; ++w) mine[w] = 0;
-            uint32_t word = 0;
-            int at = j >> 5;
-            for (int a = j; a >= 0; a = s_parent[a]) {
-              if (a >> 5 != at) {
-                mine[at] = word;
-                word = 0;
-                at = a >> 5;
-              }
-              word |= 1u << (a & 31);
-            }
-            mine[at] = word;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::ANC_FULL + a2));
-          built = true;
-        }
         const uint32_t u = units + unit_v(t, nt);
         if (!(ok = wait_slot(C::V_FULL, u % C::STAGES, v_phase))) break;
         uint8_t* v = bp + C::RING + (u % C::STAGES) * C::UNIT + f * ROWS * 32;
@@ -691,33 +698,63 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       const int r0 = y.mt * kTreeRows, j = min(r0 + r, y.n * group - 1) / group;
       return ((size_t)(y.lo + j) * p.num_query_heads + y.g * group + (r0 + r - j * group)) * D;
     };
-    // QR pieces of this thread's query row from piece `first` of its QN on;
-    // zeros past the last row.  Pieces of a row: for TMEM a run per group, for
-    // shared memory every NG-th.
-    auto load_query = [&](const Segment& y, int first, uint4 (&e)[C::QR]) {
+    // A warp fetches the group's part of its 32 query rows, zeros past the last
+    // row, in loads that cover 32 / QP rows each: a thread that reads its own
+    // row touches 32 lines with every load (D = 256: 4500 clocks instead of
+    // 1500 for a row tile).  Load i: pieces QP (i / QP) on, rows i % QP on.
+    const int q_piece = C::QP == 8 ? lane & 7 : lane >> 3;
+    const int q_row = C::QP == 8 ? lane >> 3 : lane & 7;
+    constexpr uint32_t kNoRow = 0xffffffffu;  // (as many rows do not fit the memory)
+    auto load_query = [&](const Segment& y, uint4 (&e)[C::QN]) {
       const int rows = rows_of(y), r = row % span_of(rows);
-      const uint4* src =
-          reinterpret_cast<const uint4*>(static_cast<const T*>(p.query) + row_at(y, r));
+      const uint32_t mine = r < rows ? (uint32_t)(row_at(y, r) / D) : kNoRow;
+      const uint4* q = static_cast<const uint4*>(p.query) + grp * C::QN + q_piece;
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < C::QR; ++i)
-        e[i] = r < rows ? __ldg(src + (C::Q_TMEM ? grp * C::QN + first + i : grp + NG * (first + i)))
-                        : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < C::QP; ++k) {
+        const uint32_t at = __shfl_sync(0xffffffffu, mine, k * (32 / C::QP) + q_row);
+#pragma unroll
+        for (int i = k; i < C::QN; i += C::QP)
+          e[i] = at != kNoRow ? __ldg(q + (size_t)at * (D / 8) + i / C::QP * C::QP)
+                              : make_uint4(0, 0, 0, 0);
+      }
     };
-    auto store_query = [&](int first, const uint4 (&e)[C::QR]) {
+    auto store_query = [&](const uint4 (&e)[C::QN]) {
       if constexpr (C::Q_TMEM) {
-        __syncwarp();
+        // Rows meet their threads in the group's stage, each in the words that
+        // it alone writes there later (128 bytes of every 512, pieces exchanged
+        // against bank conflicts).
+        uint8_t* at = reinterpret_cast<uint8_t*>(stage) + (warp & 3) * 128;
 #pragma unroll
-        for (int i = 0; i < C::QR; i += 4) {
-          const uint32_t w[16] = {e[i].x,     e[i].y,     e[i].z,     e[i].w,
-                                  e[i + 1].x, e[i + 1].y, e[i + 1].z, e[i + 1].w,
-                                  e[i + 2].x, e[i + 2].y, e[i + 2].z, e[i + 2].w,
-                                  e[i + 3].x, e[i + 3].y, e[i + 3].z, e[i + 3].w};
-          tmem_st16(tmem + lanes + C::QT() + 4 * (grp * C::QN + first + i), w);
+        for (int i0 = 0; i0 < C::QN; i0 += C::QP) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < C::QP; ++i) {
+            const int q = i * (32 / C::QP) + q_row;
+            *reinterpret_cast<uint4*>(at + q * 512 + ((q_piece ^ q) & 7) * 16) = e[i0 + i];
+          }
+          __syncwarp();
+          uint4 o[C::QP];
+#pragma unroll
+          for (int i = 0; i < C::QP; ++i)
+            o[i] = *reinterpret_cast<const uint4*>(at + lane * 512 + ((i ^ lane) & 7) * 16);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < C::QP; i += 4) {
+            const uint32_t w[16] = {o[i].x,     o[i].y,     o[i].z,     o[i].w,
+                                    o[i + 1].x, o[i + 1].y, o[i + 1].z, o[i + 1].w,
+                                    o[i + 2].x, o[i + 2].y, o[i + 2].z, o[i + 2].w,
+                                    o[i + 3].x, o[i + 3].y, o[i + 3].z, o[i + 3].w};
+            tmem_st16(tmem + lanes + C::QT() + 4 * (grp * C::QN + i0 + i), w);
+          }
         }
+        __syncwarp();
       } else {
-        uint4* dst = reinterpret_cast<uint4*>(bp + C::Q) + row;
+        uint4* dst = reinterpret_cast<uint4*>(bp + C::Q) + (row & ~31);
 #pragma unroll
-        for (int i = 0; i < C::QR; ++i) dst[(grp + NG * (first + i)) * kTreeRows] = e[i];
+        for (int i = 0; i < C::QN; ++i)
+          dst[(grp * C::QN + i / C::QP * C::QP + q_piece) * kTreeRows +
+              (i % C::QP) * (32 / C::QP) + q_row] = e[i];
       }
     };
     auto query_ready = [&]() {
@@ -738,20 +775,23 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         if (lane == 0) *s_go = go ? 1 : 0;
       }
     };
+    uint4 query[C::QN];
     take_segment(0);
     softmax_barrier(1, C::SOFTMAX);
     bool more = *s_go != 0;
-    uint4 query[C::QR];
-    if (more) load_query(segs[0], 0, query);
+    if (more) {
+      load_query(segs[0], query);
+      if (C::Q_TMEM) {
+        store_query(query);
+        query_ready();
+      }
+    }
     while (more) {
       x = segs[count % kSegDepth];
-      store_query(0, query);
-#pragma unroll 1
-      for (int i = C::QR; i < C::QN; i += C::QR) {
-        load_query(x, i, query);
-        store_query(i, query);
+      if (!C::Q_TMEM) {
+        store_query(query);
+        query_ready();
       }
-      query_ready();
       const int nt = x.t1 - x.t0;
       const int r0 = x.mt * kTreeRows;  // row r of the tile is row r0 + r of the sequence
       const int rows = rows_of(x);
@@ -922,21 +962,6 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::P_READY + b));
       }
-      // the group's last product
-      if (NG == 2) {
-        const int mine = (nt - grp + 1) / 2;  // the group's tiles
-        if (mine > 0) {
-          // products of one buffer finish in order: all but the last are
-          // known to be over (see above)
-          pv_count ^= (uint32_t)((mine - 1) & 1) << grp;
-          if (ok) ok = wait(C::PV_DONE + grp, pv_count >> grp & 1u);
-          pv_count ^= 1u << grp;
-        }
-      } else {
-        const int b = (nt - 1) & 1;
-        if (ok) ok = wait(C::PV_DONE + b, pv_count >> b & 1u);
-        pv_count ^= 1u << b;
-      }
       // -1 marks a row that sees keys, all with a score of -inf
       if (m == -INFINITY && l == 0.f && seen) l = -1.f;
       s_ml[(grp * 2 + 0) * kTreeRows + row] = m;
@@ -945,7 +970,26 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       softmax_barrier(1, C::SOFTMAX);
       if (warp == 0) release_segment();  // all have read x
       more = *s_go != 0;
-      if (more) load_query(segs[(count + 1) % kSegDepth], 0, query);  // in flight from here on
+      if (more) {
+        // All scores of this segment are there, so the next one's query rows
+        // can go to TMEM: its first products run under this one's output.
+        load_query(segs[(count + 1) % kSegDepth], query);
+        if (C::Q_TMEM) {
+          tc_fence_after();
+          store_query(query);
+          query_ready();
+        }
+      }
+      // The last products.  Those of one buffer finish in order, and all but
+      // its last are known to be over (see above).
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int those = (nt - b + 1) / 2;  // the buffer's tiles
+        if (NG == 1 ? b != ((nt - 1) & 1) : those == 0) continue;
+        if (NG == 2) pv_count ^= (uint32_t)((those - 1) & 1) << b;
+        if (ok) ok = wait(C::PV_DONE + b, pv_count >> b & 1u);
+        pv_count ^= 1u << b;
+      }
       // m, l of the row over groups and copies, and this thread's factors
       float mm = -INFINITY, ll = 0.f, f[NG];
       bool nan = false, weightless = false;
