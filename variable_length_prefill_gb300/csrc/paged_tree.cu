@@ -1122,10 +1122,13 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         if (lane == 0) mbar_arrive(bar(C::ANC_EMPTY + a2));
         ++uses;
       }
-      if (!whole && x.t0 == 0) {
-        const long long next = x.u + x.nt + TreeCfg<D>::OVERHEAD;  // the unit behind the row tile
-        open = {1, x.lo, x.n, x.g, x.mt,
-                (int)((next * range.used + range.total - 1) / range.total) - 1, {0, 0}};
+      if (x.t1 < x.nt) {
+        // the CTAs that hold the row tile's first key tile and its last unit
+        auto holder = [&](long long u) {
+          return (int)(((u + 1) * range.used + range.total - 1) / range.total) - 1;
+        };
+        open = {1, x.lo, x.n, x.g, x.mt, holder(x.u + C::OVERHEAD + x.nt - 1),
+                holder(x.u + C::OVERHEAD), 0};
       }
       tiles += nt;
       ++count;
@@ -1146,60 +1149,75 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the partial results of the row tile that CTA blockIdx.x began and
-// others went on with: 32 rows (blockIdx.y) and 64 columns (blockIdx.z) a CTA,
-// a row a lane, 8 columns a warp, the parts in CTA order.  A few dozen parts
-// are read one behind the other, so what counts is loads in flight: the parts'
-// factors are found first, by all warps, and kJoinParts parts are read at
-// a time (one by one, a tile of 30 parts took 60 us).
+// Joins the partial results of the row tiles that no CTA holds whole.  A row tile
+// of two or three parts is bound by L2; one of a hundred (a long sequence by
+// itself) by latency, so what counts is loads in flight.  A CTA joins 32 rows (a
+// row a lane) and 64 columns, 8 columns a warp, or 1 / 2, 1 / 4, 1 / 8 of the
+// columns with the parts dealt out to as many groups of warps, so that no warp
+// reads more than a few rounds of kJoinParts parts: then CTAs that stand for
+// the attention CTAs in the middle of the row tile join the other columns.  The
+// parts of a group are added in CTA order and the groups in theirs.  (One token
+// on one sequence of 100000: 89 us without groups, 36 with them.)
 constexpr int kJoinThreads = 256;
-constexpr int kJoinCols = 64;
+constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinParts = 4;
 
+// groups of warps that share the parts of a row tile: fewer than parts
+__device__ __forceinline__ int join_groups(int parts) {
+  return parts <= kJoinParts ? 1 : (parts <= 2 * kJoinParts ? 2 : (parts <= 4 * kJoinParts ? 4 : 8));
+}
+
 template <int D, typename T>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeParams p) {
-  __shared__ float s_m[kJoinThreads / 32][32], s_l[kJoinThreads / 32][32];
+__global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid_constant__ TreeParams p) {
+  __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32];
   __shared__ float s_f[kTreeMaxCtas][32];
-  constexpr int WARPS = kJoinThreads / 32;
+  __shared__ float s_o[kJoinWarps][8][32];
   grid_wait_prerequisite();
-  const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const TreeOpen open = reinterpret_cast<const TreeOpen*>(p.workspace)[cta];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = p.num_query_heads / p.c.num_kv_heads;
-  const int r0 = open.mt * kTreeRows, row = 32 * blockIdx.y + lane;
-  const int rows = open.valid ? min(kTreeRows, open.n * group - r0) : 0;
-  if (32 * (int)blockIdx.y >= rows) return;
-  const bool live = row < rows;  // rows past the last have no partial results
+  const TreeOpen open = reinterpret_cast<const TreeOpen*>(p.workspace)[blockIdx.x];
+  if (!open.valid) return;
+  const int rows = min(kTreeRows, open.n * group - open.mt * kTreeRows);
+  const int cta = open.first, count = open.last - cta + 1, groups = join_groups(count);
+  const int share = blockIdx.x - cta;  // of this CTA's columns
+  if (32 * (int)blockIdx.y >= rows || share >= groups) return;
   const float* parts = reinterpret_cast<const float*>(p.workspace + tree_parts_offset());
+  const int across = kJoinWarps / groups;  // warps side by side on columns
+  const int row = 32 * blockIdx.y + lane;
+  const int c = ((blockIdx.z * groups + share) * across + warp % across) * 8, mine = warp / across;
+  const bool live = row < rows;  // rows past the last have no partial results
   auto part = [&](int k) {
-    return parts + (size_t)(k == cta ? 2 * cta + 1 : 2 * k) * tree_part_floats(D) + row;
+    return parts + (size_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)) * tree_part_floats(D) + row;
   };
-  const int c = blockIdx.z * kJoinCols + warp * 8, count = open.last - cta + 1;
   float e[kJoinParts][8];
   auto read = [&](int k0) {
 #pragma unroll
-    for (int x = 0; x < kJoinParts; ++x)
+    for (int x = 0; x < kJoinParts; ++x) {
+      const int k = k0 + x * groups;
+      const bool there = live && k < count;
+      const float* src = part(there ? k : 0) + c * kTreeRows;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        e[x][i] = live && k0 + x < count ? part(cta + k0 + x)[(c + i) * kTreeRows] : 0.f;
+      for (int i = 0; i < 8; ++i) e[x][i] = there ? src[i * kTreeRows] : 0.f;
+    }
   };
-  read(0);
+  read(mine);
   // the row's maximum, and the parts' factors and sums
   float mm = -INFINITY, l0 = 0.f;  // l0: the sum of this warp's first part
-  for (int k = warp; k < count; k += WARPS) {
-    const float m = live ? part(cta + k)[D * kTreeRows] : -INFINITY;
-    if (k == warp) l0 = live ? part(cta + k)[(D + 1) * kTreeRows] : 0.f;
+  for (int k = warp; k < count; k += kJoinWarps) {
+    const float m = live ? part(k)[D * kTreeRows] : -INFINITY;
+    if (k == warp) l0 = live ? part(k)[(D + 1) * kTreeRows] : 0.f;
     s_f[k][lane] = m;
     mm = fmaxf(mm, m);
   }
   s_m[warp][lane] = mm;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, s_m[w][lane]);
+  for (int w = 0; w < kJoinWarps; ++w) mm = fmaxf(mm, s_m[w][lane]);
   float ll = 0.f;
   bool nan = false, weightless = false;
-  for (int k = warp; k < count; k += WARPS) {
+  for (int k = warp; k < count; k += kJoinWarps) {
     const float m = s_f[k][lane];
-    const float l = k == warp ? l0 : (live ? part(cta + k)[(D + 1) * kTreeRows] : 0.f);
+    const float l = k == warp ? l0 : (live ? part(k)[(D + 1) * kTreeRows] : 0.f);
     const float f = m == -INFINITY ? 0.f : ex2(m - mm);
     if (f > 0.f) ll += f * l;
     nan |= !(l == l);
@@ -1210,38 +1228,49 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   s_m[warp][lane] = ll;
   s_l[warp][lane] = nan ? 2.f : (weightless ? 1.f : 0.f);
   __syncthreads();
-  ll = 0.f;
-  float state = 0.f;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    ll += s_m[w][lane];
-    state = fmaxf(state, s_l[w][lane]);
-  }
-  float scale = 1.f / ll;
-  if (state == 2.f || (mm == -INFINITY && state == 1.f)) scale = __uint_as_float(0x7fc00000u);
-  else if (mm == -INFINITY) scale = 0.f;
   float o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  for (int k = 0; k < count; k += kJoinParts) {
-    if (k) read(k);
+  for (int k0 = mine; k0 < count; k0 += kJoinParts * groups) {
+    if (k0 != mine) read(k0);
 #pragma unroll
     for (int x = 0; x < kJoinParts; ++x) {
-      if (k + x >= count) break;
-      const float f = s_f[k + x][lane];
+      const int k = k0 + x * groups;
+      if (k >= count) break;
+      const float f = s_f[k][lane];
       // a factor of 0 does not silence a value that is not finite
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         o[i] += f != 0.f ? f * e[x][i] : (e[x][i] - e[x][i] == 0.f ? 0.f : e[x][i]);
     }
   }
-  if (!live) return;
-  const int j = (r0 + row) / group;
-  T* dst = static_cast<T*>(p.out) +
-           ((size_t)(open.lo + j) * p.num_query_heads + open.g * group + (r0 + row - j * group)) * D + c;
-  *reinterpret_cast<uint4*>(dst) = make_uint4(
-      Half16<T>::pack(o[0] * scale, o[1] * scale), Half16<T>::pack(o[2] * scale, o[3] * scale),
-      Half16<T>::pack(o[4] * scale, o[5] * scale), Half16<T>::pack(o[6] * scale, o[7] * scale));
+  if (groups > 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_o[warp][i][lane] = o[i];
+    __syncthreads();
+    if (mine == 0)
+      for (int w = warp + across; w < kJoinWarps; w += across)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += s_o[w][i][lane];
+  }
+  if (mine == 0 && live) {
+    float state = 0.f;
+    ll = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      ll += s_m[w][lane];
+      state = fmaxf(state, s_l[w][lane]);
+    }
+    float scale = 1.f / ll;
+    if (state == 2.f || (mm == -INFINITY && state == 1.f)) scale = __uint_as_float(0x7fc00000u);
+    else if (mm == -INFINITY) scale = 0.f;
+    const int r = open.mt * kTreeRows + row, j = r / group;
+    T* dst = static_cast<T*>(p.out) +
+             ((size_t)(open.lo + j) * p.num_query_heads + open.g * group + (r - j * group)) * D + c;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(
+        Half16<T>::pack(o[0] * scale, o[1] * scale), Half16<T>::pack(o[2] * scale, o[3] * scale),
+        Half16<T>::pack(o[4] * scale, o[5] * scale), Half16<T>::pack(o[6] * scale, o[7] * scale));
+  }
 }
 
 template <int D, typename T>
@@ -1261,7 +1290,7 @@ cudaError_t launch_dt(const TreeParams& p, cudaStream_t stream) {
   tree_kernel<D, T><<<grid, C::THREADS, C::BYTES, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, kTreeRows / 32, D / kJoinCols);
+  cfg.gridDim = dim3(grid, kTreeRows / 32, D / 64);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};

@@ -33,13 +33,14 @@ struct TreeParams {
 // Workspace: kTreeMaxCtas TreeOpen records, then fp32 partial results
 // [2 kTreeMaxCtas][head_size + 2][kTreeRows]: O, then the maximum and the sum.
 struct TreeOpen {
-  int valid;  // a row tile that this CTA begins and leaves to others to finish
+  int valid;  // a row tile that this CTA works on and leaves to others to finish
   int lo;     // first packed row of its sequence
   int n;      // drafts
   int g;      // KV head
   int mt;     // row tile
   int last;   // the CTA that finishes it
-  int pad[2];
+  int first;  // the CTA that began it
+  int pad;
 };
 
 __host__ __device__ constexpr size_t tree_parts_offset() { return sizeof(TreeOpen) * kTreeMaxCtas; }
