@@ -63,10 +63,12 @@ __global__ void __launch_bounds__(kWriteThreads, 4) cache_write_kernel(
   __shared__ UnitScratch scratch;
   const int groups = (p.c.num_kv_heads + head_group - 1) / head_group;
   const UnitRange range = locate_units<kWriteThreads>(
-      p.c.num_seqs, blockIdx.x, gridDim.x, 1, scratch, [&](int i) -> long long {
+      p.c.num_seqs, blockIdx.x, gridDim.x, scratch,
+      [&](int i) -> Units {
         const NewTokens t = new_tokens(p.cu, p.seq_lens, i, p.total_tokens);
-        return (long long)write_pages(t, p.c.max_blocks).pages * groups;
-      });
+        return {(long long)write_pages(t, p.c.max_blocks).pages * groups, 1};
+      },
+      [](int) { return 1; });
   const int tid = threadIdx.x;
   const int pieces = p.c.head_size / 8;  // 16-byte pieces of a head's elements, a power of two
   const int shift = __ffs(pieces) - 1;

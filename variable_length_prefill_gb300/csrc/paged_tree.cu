@@ -100,14 +100,23 @@ struct TreeCfg {
   static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? 5 : 6);
   static constexpr int SOFTMAX = 128 * NG;  // softmax threads
   // A row tile's fixed cost (query rows in, filling the pipeline, output) in key
-  // tiles, for the CTAs' equal shares.  Counted as 3 / 6 / 10 / 15 tiles, 16
-  // sequences of up to 2112 tokens and 64 drafts at D = 256 took 66 / 55 / 51 /
-  // 52 us, and 64 x 4096 tokens at D = 128 186 / 185 / 187 / 189.
-  static constexpr int OVERHEAD = D == 256 ? 10 : 6;
-  // No share is smaller: below that, one more CTA on a row tile saves less than
-  // its partial results cost to join (5 sequences of up to 3239 tokens and one
-  // KV head: 28 us without a least share, 20 us with 4, 23 with 8, 27 with 12).
-  static constexpr int LEAST = OVERHEAD - 2;
+  // tiles, for the CTAs' equal shares.  Counted as 5 / 7 / 8 / 10 tiles, 16
+  // sequences of up to 2112 tokens and 64 drafts at D = 256 took 51.8 / 47.7 /
+  // 48.4 / 48.2 us; counted as 3 / 4 / 5 / 6, at D = 128 with 8 KV heads 47.8 /
+  // 41.2 / 43.2 / 40.9, and 5 of up to 3239 with one KV head 16.5 / 16.5 / 16.3 /
+  // 19.1 (64 x 4096 tokens: no difference).
+  static constexpr int OVERHEAD = D == 256 ? 8 : 4;
+  // No share is smaller than this, nor than least(): more CTAs on a row tile
+  // leave more partial results to join.  At D = 128 a first turn (4 x 128 tokens)
+  // took 12.6 us with 2 and 13.0 with 4, 5 x 3239 tokens 16.5 and 17.8.
+  static constexpr int LEAST = D == 256 ? 4 : 2;
+  // s units a share take time as s, and the parts of a row tile of m units as
+  // m / s, least together at s ~ sqrt(m).  One token on 20000 / 100000 at D = 64:
+  // 16.9 / 27.6 us with m / 5 under the root, 17.0 / 26.3 with m / 10, 18.3 /
+  // 25.7 with m / 20, 16.6 / 34 with 4 units for both.
+  __device__ static int least(int longest) {
+    return max(LEAST, (int)sqrtf(0.1f * (float)longest));
+  }
   static constexpr int THREADS = SOFTMAX + 128;
   // Warps past the softmax groups
   static constexpr int FIX = 4 * NG, PROD = 4 * NG + 2, MMA = 4 * NG + 3;
@@ -273,6 +282,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   constexpr int NT = C::NT, NG = C::NG, BLK = C::BLK;
   extern __shared__ uint8_t smem_raw[];
   __shared__ UnitScratch scratch;
+  __shared__ long long s_total;  // of the range, for the end of a segment
+  __shared__ int s_used;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* bp = smem_raw + (base - raw);
@@ -313,10 +324,17 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   }
   const int group = p.num_query_heads / p.c.num_kv_heads;
   const UnitRange range = locate_units<C::THREADS>(
-      p.c.num_seqs, blockIdx.x, gridDim.x, C::LEAST, scratch, [&](int i) -> long long {
+      p.c.num_seqs, blockIdx.x, gridDim.x, scratch,
+      [&](int i) -> Units {
         const SeqInfo s = seq_info<D>(p, group, i);
-        return (long long)s.mts * p.c.num_kv_heads * (s.nt + TreeCfg<D>::OVERHEAD);
-      });
+        const int per = s.nt + C::OVERHEAD;
+        return {(long long)s.mts * p.c.num_kv_heads * per, s.mts ? per : 0};
+      },
+      [](int longest) { return C::least(longest); });
+  if (tid == 0) {
+    s_total = range.total;
+    s_used = range.used;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1124,9 +1142,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       }
       if (x.t1 < x.nt) {
         // the CTAs that hold the row tile's first key tile and its last unit
-        auto holder = [&](long long u) {
-          return (int)(((u + 1) * range.used + range.total - 1) / range.total) - 1;
-        };
+        const long long total = s_total, used = s_used;
+        auto holder = [&](long long u) { return (int)(((u + 1) * used + total - 1) / total) - 1; };
         open = {1, x.lo, x.n, x.g, x.mt, holder(x.u + C::OVERHEAD + x.nt - 1),
                 holder(x.u + C::OVERHEAD), 0};
       }

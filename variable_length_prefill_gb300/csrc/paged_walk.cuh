@@ -19,8 +19,16 @@ struct UnitRange {
   int seq;
 };
 
+// The units of a sequence, and how many of them its longest piece of work has
+// (pieces are the caller's: what a range that ends inside one costs extra for).
+struct Units {
+  long long count;
+  int longest;
+};
+
 struct UnitScratch {
   long long warp_sum[32];
+  int warp_longest[32];
   long long off;
   int seq;
 };
@@ -34,21 +42,30 @@ __device__ __forceinline__ long long warp_inclusive(long long x, int lane) {
   return x;
 }
 
-// Range `part` of at most `parts`, none shorter than `least` units unless there
-// are fewer; every thread of the CTA takes part.  count(i) is the units of
-// sequence i.  Thread t sums a run of consecutive sequences, a
+// Range `part` of at most `parts`, none shorter than least(longest piece of all)
+// units unless there are fewer; every thread of the CTA takes part.  units(i)
+// is the Units of sequence i.  Thread t sums a run of consecutive sequences, a
 // scan over the threads gives the total, and the thread whose run holds unit
 // u0 walks it.
-template <int THREADS, class Count>
-__device__ __forceinline__ UnitRange locate_units(int n, int part, int parts, int least,
-                                                  UnitScratch& s, Count count) {
+template <int THREADS, class Count, class Least>
+__device__ __forceinline__ UnitRange locate_units(int n, int part, int parts, UnitScratch& s,
+                                                  Count units, Least least) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (n + THREADS - 1) / THREADS;
   const int a = min(n, tid * run), b = min(n, a + run);
   long long sum = 0;
-  for (int i = a; i < b; ++i) sum += count(i);
+  int longest = 0;
+  for (int i = a; i < b; ++i) {
+    const Units x = units(i);
+    sum += x.count;
+    longest = max(longest, x.longest);
+  }
   const long long inc = warp_inclusive(sum, lane);
-  if (lane == 31) s.warp_sum[warp] = inc;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    s.warp_sum[warp] = inc;
+    s.warp_longest[warp] = longest;
+  }
   if (tid == 0) {
     s.seq = n;
     s.off = 0;
@@ -59,9 +76,10 @@ __device__ __forceinline__ UnitRange locate_units(int n, int part, int parts, in
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += s.warp_sum[w];
     total += s.warp_sum[w];
+    longest = max(longest, s.warp_longest[w]);
   }
   // ranges that hold units
-  const int used = (int)min((long long)parts, max(total / least, min(total, 1LL)));
+  const int used = (int)min((long long)parts, max(total / least(longest), min(total, 1LL)));
   UnitRange r;
   r.total = total;
   r.used = used;
@@ -70,7 +88,7 @@ __device__ __forceinline__ UnitRange locate_units(int n, int part, int parts, in
   if (r.u0 < r.u1 && before <= r.u0 && r.u0 < before + sum) {
     long long at = before;
     for (int i = a; i < b; ++i) {
-      const long long c = count(i);
+      const long long c = units(i).count;
       if (r.u0 < at + c) {
         s.seq = i;
         s.off = r.u0 - at;
