@@ -285,6 +285,20 @@ def test_fork_long_row_and_bad_pages(cuda_lib):
     _same(dev[:2], (k, v))
 
 
+@pytest.mark.parametrize("rows", [0, 3])
+def test_nothing_to_fork_or_free(cuda_lib, rows):
+    rng = np.random.default_rng(31)
+    k, v = ref.new_caches(rng, 4, 2, 64)
+    gk, gv, none = _bf16(k), _bf16(v), _t(np.zeros(0, dtype=np.int32))
+    tables, lens = np.zeros((rows, 2), dtype=np.int32), np.zeros(rows, dtype=np.int32)
+    refs = _t(np.ones(4, dtype=np.int32))
+    cuda_lib.paged_attn_cache_fork(gk, gv, _t(tables), _t(lens), refs, none, none)
+    cuda_lib.paged_attn_cache_free(_t(tables), _t(lens), refs, none)
+    _raises(cuda_lib)
+    np.testing.assert_array_equal(_bits(gk), k)
+    assert (refs.cpu().numpy() == 1).all()
+
+
 def test_free(cuda_lib):
     rng = np.random.default_rng(35)
     k, v, tables, lens, refs = _pool(rng, 9, [40, 48, 1, 0, 16, 300], 3)

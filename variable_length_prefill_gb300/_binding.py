@@ -287,15 +287,22 @@ def chunk_delta_rule_output(q, k, v, h, g, chunk_size=64, scale=None, out=None, 
 # A call for another device or stream than the current ones runs again with
 # those made current, so that what it allocates belongs to them.
 def _torch():
-    global _torch_module, _i32, _types, _raw_stream
+    global _torch_module, _i32, _types, _raw_stream, _device, _take, _give
     import torch
     _torch_module, _i32, _types = torch, torch.int32, (torch.bfloat16, torch.float16)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    # memory of the caching allocator, on the current device, without a tensor
+    # around it (which costs the host 6 us more)
+    _take = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None) or (
+        lambda n, stream: torch.cuda.caching_allocator_alloc(n, None, stream))
+    _give = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None) or \
+        torch.cuda.caching_allocator_delete
     return torch
 
 
-_torch_module = _i32 = _types = _raw_stream = None
+_torch_module = _i32 = _types = _raw_stream = _device = _take = _give = None
 
 
 def _ints(t, shape, dev, name):
@@ -336,7 +343,7 @@ def _elsewhere(dev, stream):
     """A context that makes the call's device and stream current; None if they are."""
     cuda = _torch_module.cuda
     if stream is None:
-        return None if cuda.current_device() == dev else cuda.device(dev)
+        return None if _device() == dev else cuda.device(dev)
     if stream.device.index != dev:
         raise ValueError(f"the stream belongs to CUDA device {stream.device.index}, the tensors "
                          f"to {dev}")
@@ -346,10 +353,6 @@ def _elsewhere(dev, stream):
 @functools.lru_cache(maxsize=1024)
 def _workspace_bytes(name, *sizes):
     return getattr(load(), f"{name}_workspace_size")(*sizes)
-
-
-def _bytes(n, dev):
-    return _torch_module.empty(n, dtype=_torch_module.uint8, device=dev)
 
 
 def _done(rc, where):
@@ -473,11 +476,16 @@ def paged_attn_cache_fork(k_cache, v_cache, block_tables, seq_lens, refs, src, d
             return paged_attn_cache_fork(k_cache, v_cache, block_tables, seq_lens, refs, src, dst)
     lib = _LIB or load()
     size = _workspace_bytes("paged_attn_cache_fork", n, s)
-    ws = _bytes(size, dev)
-    _done(lib.paged_attn_cache_fork(
-        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-        refs.data_ptr(), src.data_ptr(), dst.data_ptr(), n, s, hkv, d, bs, w, nb, ws.data_ptr(),
-        size, _raw_stream(dev)), "paged_attn_cache_fork")
+    queue = _raw_stream(dev)
+    ws = _take(size, queue)
+    try:
+        rc = lib.paged_attn_cache_fork(
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+            refs.data_ptr(), src.data_ptr(), dst.data_ptr(), n, s, hkv, d, bs, w, nb, ws, size,
+            queue)
+    finally:
+        _give(ws)  # later calls on the stream may have it
+    _done(rc, "paged_attn_cache_fork")
 
 
 def paged_attn_cache_compact(k_cache, v_cache, block_tables, seq_lens, refs, out=None, stream=None):
@@ -504,11 +512,16 @@ def paged_attn_cache_compact(k_cache, v_cache, block_tables, seq_lens, refs, out
         _ints(refs_out, (nb,), dev, "out refs")
     lib = _LIB or load()
     size = _workspace_bytes("paged_attn_cache_compact", nb)
-    ws = _bytes(size, dev)
-    _done(lib.paged_attn_cache_compact(
-        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-        refs.data_ptr(), s, hkv, d, bs, w, nb, tables_out.data_ptr(), refs_out.data_ptr(),
-        ws.data_ptr(), size, _raw_stream(dev)), "paged_attn_cache_compact")
+    queue = _raw_stream(dev)
+    ws = _take(size, queue)
+    try:
+        rc = lib.paged_attn_cache_compact(
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+            refs.data_ptr(), s, hkv, d, bs, w, nb, tables_out.data_ptr(), refs_out.data_ptr(), ws,
+            size, queue)
+    finally:
+        _give(ws)  # later calls on the stream may have it
+    _done(rc, "paged_attn_cache_compact")
     return tables_out, refs_out
 
 
@@ -548,13 +561,17 @@ def paged_attn_tree(query, k_cache, v_cache, block_tables, seq_lens, cu_seqlens,
                                    parents, scale or None, out)
     lib = _LIB or load()
     size = _workspace_bytes("paged_attn_tree", d)
-    ws = _bytes(size, dev)
     if out is None:
         out = _torch_module.empty_like(query)
-    _done(lib.paged_attn_tree(
-        query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        seq_lens.data_ptr(), cu_seqlens.data_ptr(),
-        None if parents is None else parents.data_ptr(), s, total, hq, hkv, d, bs, w, nb, scale,
-        1 if dtype is _types[1] else 0, out.data_ptr(), ws.data_ptr(), size, _raw_stream(dev)),
-        "paged_attn_tree")
+    queue = _raw_stream(dev)
+    ws = _take(size, queue)
+    try:
+        rc = lib.paged_attn_tree(
+            query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            seq_lens.data_ptr(), cu_seqlens.data_ptr(),
+            None if parents is None else parents.data_ptr(), s, total, hq, hkv, d, bs, w, nb, scale,
+            1 if dtype is _types[1] else 0, out.data_ptr(), ws, size, queue)
+    finally:
+        _give(ws)  # later calls on the stream may have it
+    _done(rc, "paged_attn_tree")
     return out
