@@ -145,6 +145,32 @@ def test_few_long_sequences(cuda_lib):
     Case([(3100, 9)], 4, 1, 256, seed=8).check(cuda_lib)
 
 
+# one sequence by itself: its row tiles are split over 2 to about 70 CTAs, and
+# their parts joined by one to eight groups of warps
+PARTS = [250, 700, 1300, 2600, 6000, 21000]
+
+
+@pytest.mark.parametrize("ctx", PARTS)
+@pytest.mark.parametrize("hq,hkv,d,dtype,n", [(3, 1, 64, "bf16", 3), (8, 1, 128, "fp16", 5),
+                                              (10, 2, 128, "bf16", 33), (8, 1, 256, "bf16", 20)])
+def test_parts_of_one_long_sequence(cuda_lib, ctx, hq, hkv, d, dtype, n):
+    c = Case([(ctx, n)], hq, hkv, d, dtype, seed=32)
+    c.compare(_wide(c.run(cuda_lib), dtype), want=_dense(c))
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(4, 1, 64, "fp16"), (8, 1, 128, "bf16"),
+                                            (4, 1, 256, "bf16")])
+def test_nonfinite_context_in_one_of_many_parts(cuda_lib, hq, hkv, d, dtype):
+    c = Case([(6000, 3), (9, 2)], hq, hkv, d, dtype, seed=33)
+    nan, inf = (0x7FC0, 0x7F80) if dtype == "bf16" else (0x7E00, 0x7C00)
+    c.v[c.tables[0, 100], 0, 4, 3] = nan
+    c.v[c.tables[0, 200], 0, 7, 9] = inf
+    c.v[c.tables[0, 300], 0, d - 1, 15] = inf
+    got = c.check(cuda_lib)[:3]
+    assert np.isnan(got[:, :, 4]).all() and np.isposinf(got[:, :, [7, d - 1]]).all()
+    assert np.isfinite(np.delete(got, [4, 7, d - 1], axis=2)).all()
+
+
 def _dense(c, scale=None):
     """ref.tree on the GPU, a (sequence, KV head) at a time, for finite inputs."""
     import torch
