@@ -18,7 +18,7 @@
 //   values  a page is [D][16 tokens], 32 bytes a row: the K-major operand of one
 //           16-token step of O += P V in the 32-byte swizzle, but for the
 //           swizzle itself, which exchanges the two halves of the rows d with
-//           bit 2 set.  One bulk copy per page, and two warps exchange those
+//           bit 2 set.  One bulk copy per page, and a warp exchanges those
 //           halves in shared memory.  (A tiled copy can do the swizzle, in
 //           32-byte rows; it held the 64 x 4096 case to 322 us.)
 // P is rounded to the cache type and written to TMEM over its scores, in token
@@ -30,9 +30,13 @@
 // and end in one CTA are written to `out`; the others leave unnormalised partial
 // results in the workspace for tree_join_kernel, which adds them in CTA order:
 // results do not depend on timing.  Warps of a CTA:
-//   producer      walks the CTA's range, publishes its segments (a row tile's
-//                 key tiles in this CTA) and streams their pages through a ring;
-//   two warps     ready the values (below) and build the table of ancestors;
+//   key producer  walks the CTA's range, publishes its segments (a row tile's
+//                 key tiles in this CTA) and streams their keys through a ring;
+//   value producer  does the same for the values (a page's copy takes a warp 182
+//                 clocks to issue, whatever its size; one warp for both took
+//                 137 us instead of 113 for 64 x 4096 tokens at D = 64);
+//   value warp    readies the values (below) and builds the table of ancestors
+//                 (two warps for D = 256);
 //   MMA issuer    one elected lane;
 //   softmax       NG groups of four warps, one thread per row.
 // For D <= 128 the two groups take the key tiles in turn, each with its own
@@ -51,18 +55,18 @@
 // cache; a tile's softmax took 4000 clocks instead of 1300.
 //
 // A weight of 0 does not silence a NaN or an infinity in the values, so in a
-// tile that holds drafts or slots past the last token, the warps that ready the
-// values clear those slots, and the non-finite values of drafts; rows that see
+// tile that holds drafts or slots past the last token, the warp that readies the
+// values clears those slots, and the non-finite values of drafts; rows that see
 // one get it back at the end.
 //
 // Measured (both kernels of a call, captured; 32 query and 8 KV heads, D = 128
-// unless said): 64 x 4096 tokens, 16 drafts 185 us, 5.9 TB/s, 87 % of a copy's
-// bandwidth.  3 sequences of up to 131071, 33 drafts, 40 query heads 223 us,
-// 5.2 TB/s: tiles of 128 rows take 2000 .. 2400 clocks, scores, softmax and
-// value product one behind the other, tensor pipe 40 % busy.  16 of up to 2112,
-// 64 drafts, 4 KV heads, D = 256 48.5 us, tensor pipe 25 % busy: 1800 clocks a
-// 64-key tile (1060 of products) and 20000 for a row tile's start and end.
-// 4 x 128 tokens, 8 drafts 12.7 us, all latency.
+// unless said): 64 x 4096 tokens, 16 drafts 186 us, 5.9 TB/s, 87 % of a copy's
+// bandwidth (D = 64: 113 us, 71 %).  3 sequences of up to 131071, 33 drafts, 40
+// query heads 214 us, 5.4 TB/s: tiles of 128 rows take about 2000 clocks,
+// scores, softmax and value product one behind the other, tensor pipe 40 % busy.
+// 16 of up to 2112, 64 drafts, 4 KV heads, D = 256 49.5 us, tensor pipe 25 %
+// busy: 1800 clocks a 64-key tile (1060 of products) and 20000 for a row tile's
+// start and end.  4 x 128 tokens, 8 drafts 12.9 us, all latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -106,7 +110,10 @@ struct TreeCfg {
   static constexpr int CHUNKS = NT / 32;
   static constexpr uint32_t PAGE = D * kPageTokens * 2;  // bytes of one head's keys (or values)
   static constexpr uint32_t UNIT = BLK * PAGE;           // a key or value tile
-  static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? 5 : 6);
+  // Slots of the rings of keys and of values, which are held longer (D = 128, 3
+  // and 2: the long case takes 221 us instead of 216; D = 256, 4 and 2: 64 drafts
+  // 54 us instead of 51).
+  static constexpr int KS = D == 64 ? 5 : (D == 128 ? 2 : 3), VS = D == 64 ? 5 : 3;
   static constexpr int SOFTMAX = 128 * NG;  // softmax threads
   // A row tile's fixed cost (query rows in, filling the pipeline, output) in key
   // tiles, for the CTAs' equal shares.  Counted as 5 / 7 / 8 / 10 tiles, 16
@@ -126,12 +133,17 @@ struct TreeCfg {
   __device__ static int least(int longest) {
     return max(LEAST, (int)sqrtf(0.1f * (float)longest));
   }
-  static constexpr int THREADS = SOFTMAX + 128;
+  // Warps that ready the values.  (One, at D = 256: 16 sequences of up to 2112
+  // tokens and 64 drafts 52.6 us, not 49.5; two, at D <= 128, leave too few
+  // registers.)
+  static constexpr int NFIX = NG == 1 ? 2 : 1;
+  static constexpr int THREADS = SOFTMAX + 32 * (NFIX + 3);
   // Warps past the softmax groups
-  static constexpr int FIX = 4 * NG, PROD = 4 * NG + 2, MMA = 4 * NG + 3;
-  // the page masks of tile t are overwritten by tile t + kMaskDepth, whose
-  // keys cannot be loaded before t's values are released
-  static_assert(2 * kMaskDepth - 3 >= STAGES, "mask depth");
+  static constexpr int FIX = 4 * NG, VPROD = FIX + NFIX, KPROD = VPROD + 1, MMA = VPROD + 2;
+  // The page mask of tile t is overwritten by tile t + kMaskDepth, whose keys
+  // are loaded behind the scores of tile t + kMaskDepth - KS, which are issued
+  // behind the value product two tiles before them: t's has read the mask.
+  static_assert(kMaskDepth >= KS + 2, "mask depth");
   // TMEM columns
   __host__ __device__ static constexpr uint32_t S(int b) { return (uint32_t)(b * NT); }
   __host__ __device__ static constexpr uint32_t O(int g) { return (uint32_t)(2 * NT + g * D); }
@@ -149,23 +161,23 @@ struct TreeCfg {
   static constexpr uint32_t RING = 0;
   // query rows for D = 128, [D / 8][128 rows][16 bytes]; at the end of a segment
   // the place where copies of a row meet, [NG][kStageCols][128 rows] floats
-  static constexpr uint32_t Q = RING + STAGES * UNIT;
+  static constexpr uint32_t Q = RING + (KS + VS) * UNIT;
   static constexpr uint32_t STAGE = kStageCols * kTreeRows * 4;
   static constexpr uint32_t ANC = Q + NG * STAGE;  // [2][128][kAncStride]
   static_assert(Q_TMEM || kTreeRows * D * 2 <= NG * STAGE, "query rows");
   static constexpr uint32_t ODD = ANC + 2 * kTreeRows * kAncStride * 4;  // [2][2]
   static constexpr uint32_t PARENT = ODD + 16;
-  static constexpr uint32_t ML = PARENT + 2 * kTreeMaxDrafts * 4;  // [NG][2][128] max, sum
+  static constexpr uint32_t ML = PARENT + NFIX * kTreeMaxDrafts * 4;  // [NG][2][128] max, sum
   static constexpr uint32_t SEG = ML + NG * 2 * kTreeRows * 4;
   static_assert(SEG % 8 == 0, "segments");
   static constexpr uint32_t MASK = SEG + kSegDepth * (uint32_t)sizeof(Segment);
   static constexpr uint32_t BAR = (MASK + kMaskDepth * 4 + 7) & ~7u;
   // Barriers.  A parity wait only tells a phase from the one before it, so a
   // waiter has to see every phase of its barrier, or know that it is over: keys
-  // (waited for by the MMA issuer) and values (by the value warps) share the
-  // ring's slots and EMPTY, but not the barriers that say they have landed.
-  static constexpr int K_FULL = 0, V_FULL = STAGES, EMPTY = 2 * STAGES, V_READY = 3 * STAGES,
-                       S_FULL = 4 * STAGES,
+  // (waited for by the MMA issuer) and values (by the value warp) have rings,
+  // and barriers, of their own.
+  static constexpr int K_FULL = 0, K_EMPTY = KS, V_FULL = 2 * KS, V_READY = V_FULL + VS,
+                       V_EMPTY = V_READY + VS, S_FULL = V_EMPTY + VS,
                        P_READY = S_FULL + 2, PV_DONE = P_READY + 2, Q_READY = PV_DONE + 2,
                        ANC_FULL = Q_READY + 1, ANC_EMPTY = ANC_FULL + 2, SEG_FULL = ANC_EMPTY + 2,
                        SEG_EMPTY = SEG_FULL + kSegDepth, DRAIN = SEG_EMPTY + kSegDepth,
@@ -267,11 +279,6 @@ struct Walker {
   }
 };
 
-// Ring units of a segment with nt key tiles, in the order they are used:
-// K0 K1 V0 K2 V1 K3 ... V(nt-1).
-__device__ __forceinline__ int unit_k(int t) { return t < 2 ? t : 2 * t - 1; }
-__device__ __forceinline__ int unit_v(int t, int nt) { return t == nt - 1 ? 2 * nt - 1 : 2 * t + 2; }
-
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
@@ -300,26 +307,23 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   volatile uint32_t* page_mask = reinterpret_cast<volatile uint32_t*>(bp + C::MASK);
   Segment* segs = reinterpret_cast<Segment*>(bp + C::SEG);
   auto bar = [&](int i) { return base + C::BAR + 8u * (uint32_t)i; };
-  auto slot = [&](uint32_t unit) { return base + C::RING + (unit % C::STAGES) * C::UNIT; };
+  auto k_slot = [&](uint32_t s) { return base + C::RING + s * C::UNIT; };
+  auto v_slot = [&](uint32_t s) { return base + C::RING + (C::KS + s) * C::UNIT; };
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(bar(C::K_FULL + s), 1);
-      mbar_init(bar(C::V_FULL + s), 1);
-      mbar_init(bar(C::EMPTY + s), 1);
-      mbar_init(bar(C::V_READY + s), 2);
-    }
+    for (int i = C::K_FULL; i < C::S_FULL; ++i)  // the rings'
+      mbar_init(bar(i), i >= C::V_READY && i < C::V_EMPTY ? C::NFIX : 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(C::S_FULL + b), 1);
       mbar_init(bar(C::P_READY + b), 4);
       mbar_init(bar(C::PV_DONE + b), 1);
-      mbar_init(bar(C::ANC_FULL + b), 2);
+      mbar_init(bar(C::ANC_FULL + b), C::NFIX);
       mbar_init(bar(C::ANC_EMPTY + b), 4 * NG);
     }
     for (int s = 0; s < kSegDepth; ++s) {
       mbar_init(bar(C::SEG_FULL + s), 1);
-      mbar_init(bar(C::SEG_EMPTY + s), 4);  // MMA issuer, value warps, softmax
+      mbar_init(bar(C::SEG_EMPTY + s), C::NFIX + 3);  // all readers (the softmax as one)
     }
     mbar_init(bar(C::Q_READY), 4 * NG);
     mbar_init(bar(C::DRAIN), 1);
@@ -350,8 +354,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(bp + C::TMEM_SLOT);
   grid_launch_dependents();
   Segment x;
-  // ring units, key tiles and segments before the current segment
-  uint32_t units = 0, tiles = 0, count = 0;
+  uint32_t tiles = 0, count = 0;  // key tiles and segments before the current segment
   auto wait = [&](int b, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu,
                       wait_bounded(bar(b), parity, abort_flag, p.c.status, kPageStatusTimeout));
@@ -381,22 +384,43 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     return (long long)x.t1 * NT > x.base && x.n <= kTreeMaxDrafts;
   };
 
-  if (warp == C::PROD) {
-    // ------------------------------------------------------------ producer
-    // Page ids come 32 at a time, one read ahead of their use (a segment's
-    // first ones before the last copy of the segment before it); lane b of the
-    // warp copies page b of a tile.
-    constexpr int TPC = 32 / BLK;  // key tiles per read of ids
+  // For the producers: page ids come 32 at a time, one read ahead of their use;
+  // lane b of the warp copies page b of a tile.
+  constexpr int TPC = 32 / BLK;  // key tiles per read of ids
+  auto read_ids = [&](const Segment& y, int chunk) -> int {
+    const int i = y.t0 * BLK + chunk * 32 + lane;
+    return chunk * TPC < y.t1 - y.t0 && i < (y.len + kPageTokens - 1) / kPageTokens
+               ? __ldg(p.block_tables + (size_t)y.seq * p.c.max_blocks + i)
+               : -1;
+  };
+  // announces the pages of a tile on `full`, then copies them to `dst`; returns
+  // a bit per page that is there
+  auto copy_pages = [&](const void* cache, int page, uint32_t dst, uint32_t full,
+                        volatile uint32_t* mask_out) {
+    const bool there = lane < BLK && page >= 0 && page < p.c.num_blocks;
+    const uint32_t mask = __ballot_sync(0xffffffffu, there);
+    if (lane == 0) {
+      if (mask_out) *mask_out = mask;
+      mbar_arrive_expect_tx(full, __popc(mask) * C::PAGE);
+    }
+    __syncwarp();
+    if (there)
+      bulk_copy_g2s(dst + lane * C::PAGE,
+                    static_cast<const T*>(cache) +
+                        ((size_t)page * p.c.num_kv_heads + x.g) * (D * kPageTokens),
+                    C::PAGE, full);
+    __syncwarp();
+  };
+  // every announced copy has landed before the CTA can exit (also where others
+  // gave up); `phases` has a bit per slot
+  auto drain = [&](int full, int slots, uint32_t phases) {
+    for (int s = 0; s < slots; ++s) wait_drain(bar(full + s), (phases >> s & 1u) ^ 1u);
+  };
+
+  if (warp == C::KPROD) {
+    // -------------------------------------------------------- key producer
     Walker<D> walk{range.u0, range.u1, range.off, range.seq, -1, {}};
-    uint32_t issued = 0;
-    uint32_t k_phase = 0, v_phase = 0, is_value = 0;  // a bit per slot
-    int ids, next;
-    auto read_ids = [&](const Segment& y, int chunk) -> int {
-      const int i = y.t0 * BLK + chunk * 32 + lane;
-      return chunk * TPC < y.t1 - y.t0 && i < (y.len + kPageTokens - 1) / kPageTokens
-                 ? __ldg(p.block_tables + (size_t)y.seq * p.c.max_blocks + i)
-                 : -1;
-    };
+    uint32_t phases = 0;
     // a segment that is published soon: its query rows to L2
     auto prefetch_query = [&](const Segment& y) {
       const int r0 = y.mt * kTreeRows;
@@ -423,6 +447,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     };
     bool more = walk.next(p, group, x);
     bool ok = publish(x);
+    int ids = -1, next = -1;
     if (more) {
       ids = read_ids(x, 0);
       next = read_ids(x, 1);
@@ -431,72 +456,58 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       const int nt = x.t1 - x.t0;
       const int pages = (x.len + kPageTokens - 1) / kPageTokens;
       if (lane == 0 && x.n > kTreeMaxDrafts) atomicOr(p.c.status, kPageStatusBadDraft);
-      int id[2] = {-1, -1};  // this lane's page of the last two key tiles
-      auto issue = [&](int t, bool value) -> bool {
-        const uint32_t u = issued, s = u % C::STAGES;
-        if (!wait(C::EMPTY + s, ((u / C::STAGES) & 1u) ^ 1u)) return false;
-#if ATTN_VARLEN_TEST_HOOKS
-        if (p.test_withhold && x.u == 0 && x.t0 == 0 && u == 0) {  // not copied, not announced
-          ++issued;
-          return true;
-        }
-#endif
-        const int page = t & 1 ? id[1] : id[0];
-        const bool there = lane < BLK && page >= 0 && page < p.c.num_blocks;
-        const uint32_t mask = __ballot_sync(0xffffffffu, there);
-        const uint32_t full = bar((value ? C::V_FULL : C::K_FULL) + s);
-        (value ? v_phase : k_phase) ^= 1u << s;
-        is_value = value ? is_value | 1u << s : is_value & ~(1u << s);
-        if (lane == 0) {
-          if (!value) page_mask[(tiles + t) % kMaskDepth] = mask;
-          mbar_arrive_expect_tx(full, __popc(mask) * C::PAGE);
-        }
-        __syncwarp();
-        if (there)
-          bulk_copy_g2s(slot(u) + lane * C::PAGE,
-                        static_cast<const T*>(value ? p.c.v_cache : p.c.k_cache) +
-                            ((size_t)page * p.c.num_kv_heads + x.g) * (D * kPageTokens),
-                        C::PAGE, full);
-        __syncwarp();
-        ++issued;
-        return true;
-      };
-      auto load_k = [&](int t) -> bool {
+      __syncwarp();
+      for (int t = 0; t < nt; ++t) {
         if (t && t % TPC == 0) {
           ids = next;
           next = read_ids(x, t / TPC + 1);
         }
         const int mine = __shfl_sync(0xffffffffu, ids, (t % TPC) * BLK + lane % BLK);
-        if (t & 1) id[1] = mine; else id[0] = mine;
         if (lane < BLK && (x.t0 + t) * BLK + lane < pages && (mine < 0 || mine >= p.c.num_blocks))
           atomicOr(p.c.status, kPageStatusBadBlock);
-        return issue(t, false);
-      };
-      ok = load_k(0) && (nt < 2 || load_k(1));
-      Segment y;
-      for (int t = 0; ok && t < nt; ++t) {
-        if (t == nt - 1) {
-          more = walk.next(p, group, y);
-          if (more) {
-            ids = read_ids(y, 0);
-            next = read_ids(y, 1);
-          }
-        }
-        ok = issue(t, true);
-        if (ok && t + 2 < nt) ok = load_k(t + 2);
+        __syncwarp();
+        const uint32_t u = tiles + t, s = u % C::KS;
+        if (!(ok = wait(C::K_EMPTY + s, ((u / C::KS) & 1u) ^ 1u))) break;
+#if ATTN_VARLEN_TEST_HOOKS
+        if (p.test_withhold && x.u == 0 && x.t0 + t == 0 && u == 0) continue;  // never announced
+#endif
+        copy_pages(p.c.k_cache, mine, k_slot(s), bar(C::K_FULL + s), page_mask + u % kMaskDepth);
+        phases ^= 1u << s;
       }
       if (!ok) break;
       tiles += nt;
-      x = y;
-      if (more) prefetch_query(x);
+      more = walk.next(p, group, x);
+      if (more) {
+        ids = read_ids(x, 0);
+        next = read_ids(x, 1);
+        prefetch_query(x);
+      }
       ok = publish(x);
     }
-    // every copy has landed before the CTA can exit (also where others gave up)
-    for (uint32_t s = 0; s < min(issued, (uint32_t)C::STAGES); ++s) {
-      const bool value = is_value >> s & 1u;
-      wait_drain(bar((value ? C::V_FULL : C::K_FULL) + s),
-                 ((value ? v_phase : k_phase) >> s & 1u) ^ 1u);
+    drain(C::K_FULL, C::KS, phases);
+  } else if (warp == C::VPROD) {
+    // ------------------------------------------------------ value producer
+    uint32_t phases = 0;
+    bool ok = true;
+    while (ok && next_segment()) {
+      release_segment();
+      const int nt = x.t1 - x.t0;
+      int ids = read_ids(x, 0), next = read_ids(x, 1);
+      for (int t = 0; t < nt; ++t) {
+        if (t && t % TPC == 0) {
+          ids = next;
+          next = read_ids(x, t / TPC + 1);
+        }
+        const int mine = __shfl_sync(0xffffffffu, ids, (t % TPC) * BLK + lane % BLK);
+        const uint32_t u = tiles + t, s = u % C::VS;
+        if (!(ok = wait(C::V_EMPTY + s, ((u / C::VS) & 1u) ^ 1u))) break;
+        copy_pages(p.c.v_cache, mine, v_slot(s), bar(C::V_FULL + s), nullptr);
+        phases ^= 1u << s;
+      }
+      tiles += nt;
+      ++count;
     }
+    drain(C::V_FULL, C::VS, phases);
   } else if (warp == C::MMA) {
     // ---------------------------------------------------------- MMA issuer
     const uint32_t leader = elect_one();
@@ -510,10 +521,10 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       const int nt = x.t1 - x.t0;
       uint32_t started = 0;  // a bit per accumulator that holds something
       auto scores = [&](int t) -> bool {
-        const uint32_t u = units + unit_k(t);
-        if (!wait_slot(C::K_FULL, u % C::STAGES, k_phase)) return false;
+        const uint32_t ks = (tiles + t) % C::KS;
+        if (!wait_slot(C::K_FULL, ks, k_phase)) return false;
         tc_fence_after();
-        const uint64_t bk = smem_desc(slot(u), 256, C::PAGE, kSwizzleNone);
+        const uint64_t bk = smem_desc(k_slot(ks), 256, C::PAGE, kSwizzleNone);
         const uint32_t d = tmem + C::S(t & 1);
 #pragma unroll
         for (int half = 0; half < 2; ++half)
@@ -525,7 +536,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             else
               mma_ss_if(leader, d + half * (NT / 2), aq + ((k * 2 * 16 * kTreeRows) >> 4),
                         bk + ((half * 128 + k * 512) >> 4), id_s, k > 0 ? 1u : 0u);
-        mma_commit_if(leader, bar(C::EMPTY + u % C::STAGES));
+        mma_commit_if(leader, bar(C::K_EMPTY + ks));
         mma_commit_if(leader, bar(C::S_FULL + (t & 1)));
         return true;
       };
@@ -534,13 +545,13 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       ok = ok && scores(0) && (nt < 2 || scores(1));
       for (int t = 0; ok && t < nt; ++t) {
         const int b = t & 1, a = NG == 2 ? b : 0;
-        const uint32_t u = units + unit_v(t, nt), vs = u % C::STAGES;
+        const uint32_t vs = (tiles + t) % C::VS;
         ok = wait(C::P_READY + b, p_phase >> b & 1u) && wait_slot(C::V_READY, vs, v_phase);
         if (!ok) break;
         p_phase ^= 1u << b;
         tc_fence_after();
         const uint32_t mask = page_mask[(tiles + t) % kMaskDepth];
-        const uint64_t bv = smem_desc(slot(u), 16, 256, kSwizzle32B);
+        const uint64_t bv = smem_desc(v_slot(vs), 16, 256, kSwizzle32B);
         const uint32_t d = tmem + C::O(a), ps = tmem + C::S(b);
         if (mask == (1u << BLK) - 1u) {
           mma_ts_if(leader, d, ps, bv, id_o, started >> a & 1u);
@@ -556,25 +567,24 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             started |= 1u << a;
           }
         }
-        mma_commit_if(leader, bar(C::EMPTY + vs));
+        mma_commit_if(leader, bar(C::V_EMPTY + vs));
         mma_commit_if(leader, bar(C::PV_DONE + b));
         if (t + 2 < nt) ok = scores(t + 2);
       }
-      units += 2 * nt;
       tiles += nt;
       ++count;
     }
     // every MMA of this warp has finished before TMEM is freed
     mma_commit_if(leader, bar(C::DRAIN));
     wait_drain(bar(C::DRAIN), 0);
-  } else if (warp >= C::FIX && warp < C::FIX + 2) {
+  } else if (warp >= C::FIX && warp < C::FIX + C::NFIX) {
     // ---------------------------------------------- values made operands
-    // Each warp takes half of a tile's rows (a row: one dimension of one page,
-    // 32 bytes).  Rows with bit 2 of the dimension set exchange their halves.
+    // A row of a tile is one dimension of one page, 32 bytes.  Rows with bit 2
+    // of the dimension set exchange their halves.  Each warp has its pages.
     const int f = warp - C::FIX;
     volatile int* s_odd = reinterpret_cast<volatile int*>(bp + C::ODD);
     int* s_parent = reinterpret_cast<int*>(bp + C::PARENT) + f * kTreeMaxDrafts;
-    constexpr int ROWS = BLK * D / 2;
+    constexpr int PAGES = BLK / C::NFIX, ROWS = PAGES * D;
     uint32_t uses = 0;  // segments with drafts before this one
     uint32_t v_phase = 0;
     bool ok = true;
@@ -605,30 +615,43 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             (int)min((long long)r0 + kTreeRows - 1, (long long)x.n * group - 1) / group;
         uint32_t* table =
             reinterpret_cast<uint32_t*>(bp + C::ANC) + a2 * kTreeRows * kAncStride;
-        for (int j = j0 + f * 32 + lane; j <= last; j += 64) {
-          uint32_t* mine = table + (j - j0) * kAncStride;
+        // two drafts a lane at a time: a step of a walk is a wait for the parent
+#pragma unroll 1
+        for (int j = j0 + f * 64 + lane; j <= last; j += 64 * C::NFIX) {
+          uint32_t word[2] = {0, 0};
+          int up[2] = {j, j + 32 <= last ? j + 32 : -1}, at[2] = {j >> 5, (j + 32) >> 5};
+          uint32_t* mine[2] = {table + (j - j0) * kAncStride, table + (j + 32 - j0) * kAncStride};
 #pragma unroll
-          for (int w = 0; w < kAncWords; ++w) mine[w] = 0;
-          uint32_t word = 0;
-          int at = j >> 5;
-          for (int a = j; a >= 0; a = s_parent[a]) {
-            if (a >> 5 != at) {
-              mine[at] = word;
-              word = 0;
-              at = a >> 5;
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int w = 0; w < kAncWords; ++w)
+              if (up[i] >= 0) mine[i][w] = 0;
+          const bool both = up[1] >= 0;
+          while (up[0] >= 0 || up[1] >= 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int a = up[i];
+              if (a < 0) continue;
+              if (a >> 5 != at[i]) {
+                mine[i][at[i]] = word[i];
+                word[i] = 0;
+                at[i] = a >> 5;
+              }
+              word[i] |= 1u << (a & 31);
+              up[i] = s_parent[a];
             }
-            word |= 1u << (a & 31);
           }
-          mine[at] = word;
+          mine[0][at[0]] = word[0];
+          if (both) mine[1][at[1]] = word[1];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::ANC_FULL + a2));
       }
       for (int t = 0; t < nt; ++t) {
         const int p0 = (x.t0 + t) * NT;
-        const uint32_t u = units + unit_v(t, nt);
-        if (!(ok = wait_slot(C::V_FULL, u % C::STAGES, v_phase))) break;
-        uint8_t* v = bp + C::RING + (u % C::STAGES) * C::UNIT + f * ROWS * 32;
+        const uint32_t vs = (tiles + t) % C::VS;
+        if (!(ok = wait_slot(C::V_FULL, vs, v_phase))) break;
+        uint8_t* v = bp + C::RING + (C::KS + vs) * C::UNIT + f * ROWS * 32;
         // 16-byte pieces of the rows 4 .. 7 of every 8: 8 lanes on 128 bytes
         uint8_t* at = v + (lane >> 3) * 256 + 128 + (lane & 7) * 16;
         uint8_t* to = v + (lane >> 3) * 256 + 128 + ((lane & 7) ^ 1) * 16;
@@ -647,8 +670,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           __syncwarp();
           uint32_t odd = 0;
 #pragma unroll 1
-          for (int pg = 0; pg < BLK / 2; ++pg) {
-            const int q0 = p0 + (f * (BLK / 2) + pg) * kPageTokens;
+          for (int pg = 0; pg < PAGES; ++pg) {
+            const int q0 = p0 + (f * PAGES + pg) * kPageTokens;
             if (q0 + kPageTokens <= edge || q0 >= x.len) continue;
             // the words of a row: tokens past the last, and drafts (sign bits)
             uint32_t past[8], draft[8];
@@ -681,17 +704,19 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
                 for (int k = 0; k < 8; ++k) w[k] &= ~((wild[k] >> 15) * 0xffffu);
               }
               odd |= any;
-              *piece[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              *piece[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              if (any || q0 + kPageTokens > x.len) {
+                *piece[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                *piece[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
             }
           }
           if (odd) s_odd[2 * a2 + f] = 1;
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::V_READY + u % C::STAGES));
+        if (lane == 0) mbar_arrive(bar(C::V_READY + vs));
       }
-      units += 2 * nt;
+      tiles += nt;
       ++count;
       if (drafts) ++uses;
     }
@@ -1038,7 +1063,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       if (nan) ll = __uint_as_float(0x7fc00000u);
       if (mm == -INFINITY && !nan) ll = weightless ? -1.f : 0.f;
       // (the segment's value products are over, so its values were looked at)
-      const bool odd = drafts && (s_odd[2 * a2] | s_odd[2 * a2 + 1]) != 0;
+      const bool odd = drafts && (s_odd[2 * a2] | (C::NFIX == 2 ? s_odd[2 * a2 + 1] : 0)) != 0;
       const bool whole = x.whole();
       float scale = 1.f / ll;
       if (mm == -INFINITY) scale = ll == 0.f ? 0.f : __uint_as_float(0x7fc00000u);
