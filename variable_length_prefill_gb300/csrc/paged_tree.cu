@@ -62,7 +62,7 @@
 // Measured (both kernels of a call, captured; 32 query and 8 KV heads, D = 128
 // unless said): 64 x 4096 tokens, 16 drafts 186 us, 5.9 TB/s, 87 % of a copy's
 // bandwidth (D = 64: 113 us, 71 %).  3 sequences of up to 131071, 33 drafts, 40
-// query heads 214 us, 5.4 TB/s: tiles of 128 rows take about 2000 clocks,
+// query heads 216 us, 5.3 TB/s: tiles of 128 rows take about 2000 clocks,
 // scores, softmax and value product one behind the other, tensor pipe 40 % busy.
 // 16 of up to 2112, 64 drafts, 4 KV heads, D = 256 49.5 us, tensor pipe 25 %
 // busy: 1800 clocks a 64-key tile (1060 of products) and 20000 for a row tile's
@@ -134,8 +134,8 @@ struct TreeCfg {
     return max(LEAST, (int)sqrtf(0.1f * (float)longest));
   }
   // Warps that ready the values.  (One, at D = 256: 16 sequences of up to 2112
-  // tokens and 64 drafts 52.6 us, not 49.5; two, at D <= 128, leave too few
-  // registers.)
+  // tokens and 64 drafts 52.6 us, not 49.5 (four: 50.5); two, at D <= 128, leave
+  // too few registers.)
   static constexpr int NFIX = NG == 1 ? 2 : 1;
   static constexpr int THREADS = SOFTMAX + 32 * (NFIX + 3);
   // Warps past the softmax groups
