@@ -73,7 +73,10 @@ __global__ void __launch_bounds__(kWriteThreads, 4) cache_write_kernel(
       p.c.num_seqs, blockIdx.x, gridDim.x, scratch,
       [&](int i) -> Units {
         const NewTokens t = new_tokens(p.cu, p.seq_lens, i, p.total_tokens);
-        return {(long long)write_pages(t, p.c.max_blocks).pages * groups, 1};
+        const WritePages w = write_pages(t, p.c.max_blocks);
+        // here, not at a page: all of a sequence's tokens may lie past its table
+        if (blockIdx.x == 0 && t.n > 0 && t.len > w.end) atomicOr(p.c.status, kPageStatusBadBlock);
+        return {(long long)w.pages * groups, 1};
       },
       [](int) { return 1; });
   const int tid = threadIdx.x;
@@ -105,7 +108,6 @@ __global__ void __launch_bounds__(kWriteThreads, 4) cache_write_kernel(
     const int page = w.first + (int)(off / groups), g0 = (int)(off % groups) * head_group;
     const int heads = min(head_group, p.c.num_kv_heads - g0);
     const int id = __ldg(p.block_tables + (size_t)seq * p.c.max_blocks + page);
-    if (tid == 0 && t.len > w.end) atomicOr(p.c.status, kPageStatusBadBlock);
     if (id < 0 || id >= p.c.num_blocks) {
       if (tid == 0) atomicOr(p.c.status, kPageStatusBadBlock);
       continue;
