@@ -22,7 +22,8 @@
  * (paged_attn_decode.h).  What a row does not see has no part in it, whatever
  * it holds (NaN and infinities in unused slots or other branches included).  A
  * row that sees nothing gets zeros.  Accumulation is fp32; weights are rounded
- * to the cache type for the value product, and the output once.
+ * to the cache type for the value product (in fp16 those below 2^-32 of the
+ * row's largest may count as 0), and the output once.
  */
 #ifndef PAGED_ATTN_TREE_H_
 #define PAGED_ATTN_TREE_H_

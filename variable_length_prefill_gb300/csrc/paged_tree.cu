@@ -22,7 +22,10 @@
 //           halves in shared memory.  (A tiled copy can do the swizzle, in
 //           32-byte rows; it held the 64 x 4096 case to 322 us.)
 // P is rounded to the cache type and written to TMEM over its scores, in token
-// order, for the value product.
+// order, for the value product.  Weights are at most 2^8 of a row's running
+// maximum, so fp16 would leave seven powers of two above them unused and lose
+// those below 2^-25, which a long context has many of: fp16 weights, and with
+// them the sums, are held 2^7 times as large.
 //
 // A persistent CTA per SM takes an equal share of all (sequence, KV head, row
 // tile, key tile) units in that order (paged_walk.cuh), so a long sequence is
@@ -190,18 +193,21 @@ struct TreeCfg {
 };
 
 // The two 16-bit types: packing, the exponent that marks a NaN or an infinity,
-// and the operand format of the instruction descriptor.
+// the unit of softmax weights (2^7 times the largest, 2^8, fits fp16) and the
+// operand format of the instruction descriptor.
 template <typename T>
 struct Half16;
 template <>
 struct Half16<__nv_bfloat16> {
   static constexpr uint32_t kExp = 0x7F80u, kFormat = 1;
+  static constexpr float kWeightLog2 = 0.f;  // log2 of the unit that weights are held in
   __device__ static uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
   __device__ static float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
 };
 template <>
 struct Half16<__half> {
   static constexpr uint32_t kExp = 0x7C00u, kFormat = 0;
+  static constexpr float kWeightLog2 = 7.f;
   __device__ static uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -972,7 +978,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             }
             tmem_wait_st();
           }
-          const float off = m == -INFINITY ? 0.f : -m;
+          const float off = m == -INFINITY ? 0.f : Half16<T>::kWeightLog2 - m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
           auto weights = [&](int i, const uint32_t (&s)[32]) {
             uint32_t pk[16];
