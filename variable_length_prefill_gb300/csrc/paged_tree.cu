@@ -170,7 +170,7 @@ struct TreeCfg {
   static_assert(Q_TMEM || kTreeRows * D * 2 <= NG * STAGE, "query rows");
   static constexpr uint32_t ODD = ANC + 2 * kTreeRows * kAncStride * 4;  // [2][2]
   static constexpr uint32_t PARENT = ODD + 16;
-  static constexpr uint32_t ML = PARENT + NFIX * kTreeMaxDrafts * 4;  // [NG][2][128] max, sum
+  static constexpr uint32_t ML = PARENT + NFIX * kTreeMaxDrafts * 4;  // [NG][2][128] max (unscaled), sum
   static constexpr uint32_t SEG = ML + NG * 2 * kTreeRows * 4;
   static_assert(SEG % 8 == 0, "segments");
   static constexpr uint32_t MASK = SEG + kSegDepth * (uint32_t)sizeof(Segment);
@@ -950,10 +950,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           most(s0);
           if (two) most(s1);
           if (!masked) seen = true;
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-          // the maximum is only raised by more than 2^8 (weights stay <= 2^8)
-          const bool raise = top > m + kRescaleThreshold;
-          const float alpha = raise ? ex2(m - top) : 1.f;  // m = -inf: 0
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // the maximum (of unscaled scores) is only raised where that makes
+          // weights more than 2^8 times smaller (weights stay <= 2^8)
+          const bool raise = (top - m) * p.scale_log2 > kRescaleThreshold;
+          const float alpha = raise ? ex2((m - top) * p.scale_log2) : 1.f;  // m = -inf: 0
           if (raise) {
             m = top;
             l *= alpha;
@@ -978,7 +979,19 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             }
             tmem_wait_st();
           }
-          const float off = m == -INFINITY ? 0.f : Half16<T>::kWeightLog2 - m;
+          // A weight is 2^(scale score + off) with off the unit's less scale m.
+          // Where scale m passes 2^23, 32 bits hold scores to about 1, and what
+          // rounding leaves of scale m could be a weight that overflows.  There a
+          // power of two below the scale takes its place, whose product with m is
+          // exact (2^100 at most: scores that differ are then 2^76 apart).
+          const float ms = m * p.scale_log2;
+          float mul = p.scale_log2, off = Half16<T>::kWeightLog2 - ms;
+          if (!(fabsf(ms) < 0x1p23f)) {
+            const int e = min(__float_as_int(p.scale_log2) >> 23,
+                              127 + 227 - (__float_as_int(m) >> 23 & 255));
+            mul = __int_as_float(e << 23);
+            off = m == -INFINITY ? 0.f : __fadd_rd(Half16<T>::kWeightLog2, -(m * mul));
+          }
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
           auto weights = [&](int i, const uint32_t (&s)[32]) {
             uint32_t pk[16];
@@ -986,8 +999,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             for (int w = 0; w < 16; ++w) {
               // word w of the weights: keys 2 (w % 8), + 1 of page w / 8
               const int k = w % 8 / 4 * 16 + w / 8 * 8 + w % 4 * 2;
-              const float a = ex2(fmaf(__uint_as_float(s[k]), p.scale_log2, off));
-              const float e = ex2(fmaf(__uint_as_float(s[k + 1]), p.scale_log2, off));
+              const float a = ex2(fmaf(__uint_as_float(s[k]), mul, off));
+              const float e = ex2(fmaf(__uint_as_float(s[k + 1]), mul, off));
               sum[w % 4] += a + e;
               pk[w] = Half16<T>::pack(a, e);
             }
@@ -1060,7 +1073,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
 #pragma unroll
         for (int a = 0; a < NG; ++a) {
           const float gm = s_ml[2 * a * kTreeRows + i], gl = s_ml[(2 * a + 1) * kTreeRows + i];
-          const float e = gm == -INFINITY ? 0.f : ex2(gm - mm);
+          const float e = gm == -INFINITY ? 0.f : ex2((gm - mm) * p.scale_log2);
           if (e > 0.f) ll += e * gl;
           nan |= !(gl == gl);
           weightless |= gl == -1.f;
@@ -1275,7 +1288,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   for (int k = warp; k < count; k += kJoinWarps) {
     const float m = s_f[k][lane];
     const float l = k == warp ? l0 : (live ? part(k)[(D + 1) * kTreeRows] : 0.f);
-    const float f = m == -INFINITY ? 0.f : ex2(m - mm);
+    const float f = m == -INFINITY ? 0.f : ex2((m - mm) * p.scale_log2);
     if (f > 0.f) ll += f * l;
     nan |= !(l == l);
     weightless |= l == -1.f;

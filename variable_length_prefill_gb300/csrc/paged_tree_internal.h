@@ -31,7 +31,8 @@ struct TreeParams {
 };
 
 // Workspace: kTreeMaxCtas TreeOpen records, then fp32 partial results
-// [2 kTreeMaxCtas][head_size + 2][kTreeRows]: O, then the maximum and the sum.
+// [2 kTreeMaxCtas][head_size + 2][kTreeRows]: O, then the maximum (of scores
+// without the scale) and the sum.
 struct TreeOpen {
   int valid;  // a row tile that this CTA works on and leaves to others to finish
   int lo;     // first packed row of its sequence
