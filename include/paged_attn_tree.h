@@ -20,7 +20,8 @@
  * new tokens of a prompt, or one token (n_i = 1, plain decoding).  The cache
  * layouts, types and head sizes are those of paged_attn_decode
  * (paged_attn_decode.h).  What a row does not see has no part in it, whatever
- * it holds (NaN and infinities in unused slots or other branches included).  A
+ * it holds (NaN and infinities in unused slots or other branches included;
+ * non-finite values that rows do see cost time, up to six times as much).  A
  * row that sees nothing gets zeros.  Accumulation is fp32; weights are rounded
  * to the cache type for the value product (in fp16 those below 2^-32 of the
  * row's largest may count as 0), and the output once.

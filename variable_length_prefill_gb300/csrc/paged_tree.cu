@@ -60,7 +60,8 @@
 // A weight of 0 does not silence a NaN or an infinity in the values, so in a
 // tile that holds drafts or slots past the last token, the warp that readies the
 // values clears those slots, and the non-finite values of drafts; rows that see
-// one get it back at the end.
+// one get it back at the end, in a pass of its own over what was written
+// (mend_non_finite).
 //
 // Measured (both kernels of a call, captured; 32 query and 8 KV heads, D = 128
 // unless said): 64 x 4096 tokens, 16 drafts 186 us, 5.9 TB/s, 87 % of a copy's
@@ -295,6 +296,107 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 __device__ __forceinline__ void softmax_barrier(int id, int threads) {
   __syncwarp();
   named_bar_sync(id, threads);
+}
+
+// Sums of the non-finite values that a lane's row sees at dimensions c .. c + 7
+// among the positions [from, to), 0 where there are none.  The whole warp calls,
+// for one c.  Every row sees the whole context, so where a lane asks for it
+// (`wild`) the lanes share it, 8 tokens of a dimension a load, and add up; the
+// drafts (`branch`), at most 256, are each row's own.
+template <int D, typename T>
+__device__ __forceinline__ void non_finite_sums(const TreeParams& p, int seq, int g, int from, int to,
+                                             int base, const uint32_t* anc, int c, bool wild,
+                                             bool branch, float (&sum)[8]) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* table = p.block_tables + (size_t)seq * p.c.max_blocks;
+  const uint16_t* values = static_cast<const uint16_t*>(p.c.v_cache);
+  // adds those of the 8 tokens from pos on that `bits` names
+  auto add = [&](int id, int pos, uint32_t bits, float (&s)[8]) {
+    if (id < 0 || id >= p.c.num_blocks) return;
+    const uint4* v = reinterpret_cast<const uint4*>(
+        values + (((size_t)id * p.c.num_kv_heads + g) * D + c) * kPageTokens + pos % kPageTokens);
+    uint4 e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = __ldg(v + i * (kPageTokens / 8));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w[4] = {e[i].x, e[i].y, e[i].z, e[i].w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint16_t h = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+        if ((h & Half16<T>::kExp) == Half16<T>::kExp && (bits >> k & 1u)) s[i] += Half16<T>::widen(h);
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+  if (__any_sync(0xffffffffu, wild)) {
+    const int end = min(base, to);
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = 0.f;
+    int pos = from + 8 * lane;
+    int id = pos < end ? __ldg(table + pos / kPageTokens) : -1;
+#pragma unroll 1
+    while (pos < end) {
+      const int ahead = pos + 256;
+      const int next = ahead < end ? __ldg(table + ahead / kPageTokens) : -1;
+      add(id, pos, low_bits(end - pos), s);
+      pos = ahead;
+      id = next;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
+      if (wild) sum[i] = s[i];
+    }
+  }
+  if (branch) {
+#pragma unroll 1
+    for (int pos = max(from, base) & ~7; pos < to; pos += 8) {
+      const int a = pos - base;  // draft of the first of 8 tokens, from -7 on
+      uint32_t bits = a < 0 ? anc[0] << -a
+                            : __funnelshift_r(anc[a >> 5], a + 32 < kTreeMaxDrafts ? anc[(a >> 5) + 1] : 0u,
+                                              a & 31);
+      bits &= low_bits(to - pos) & 0xffu;
+      if (bits) add(__ldg(table + pos / kPageTokens), pos, bits, sum);
+    }
+  }
+  __syncwarp();
+}
+
+// Writes the non-finite sums of a lane's row over what stands at its columns, of
+// every output step `width` from c0 on: in the output row `dst`, or in partial
+// results.  `wild`: the steps (a bit each) where the context may hold some.  The
+// whole warp calls; rows without any have wild 0 and branch false.
+//
+// Bound by the latency of its loads.  A CTA that holds three row tiles of 131072
+// tokens each, 6 query heads' rows on one KV head, bf16, takes 5.2 ms at D = 256
+// without such values, 5.2 with some in the drafts, 11.7 with four in the context,
+// 33 with one in every dimension; at D = 128 3.0, 3.0, 5.7 and 8.7.  (Each row
+// reading all positions for itself took 190 ms for 24000 tokens, in which waits
+// of other warps could run out.)
+template <int D, typename T>
+__device__ __forceinline__ void mend_non_finite(const TreeParams& p, int seq, int g, int from, int to,
+                                             int base, const uint32_t* anc, int c0, int width,
+                                             uint32_t wild, bool branch, float scale, T* dst,
+                                             float* part) {
+#pragma unroll 1
+  for (int i = 0; i < D / TreeCfg<D>::NG / kStageCols * width; i += 8) {
+    const int step = i / width, c = c0 + step * kStageCols + i % width;
+    float sum[8];
+    non_finite_sums<D, T>(p, seq, g, from, to, base, anc, c, wild >> step & 1u, branch, sum);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (sum[k] - sum[k] == 0.f) continue;
+      if (part)
+        part[(c + k) * kTreeRows] = sum[k];
+      else
+        reinterpret_cast<uint16_t*>(dst)[c + k] = (uint16_t)Half16<T>::pack(sum[k] * scale, 0.f);
+    }
+  }
 }
 
 template <int D, typename T>
@@ -1093,34 +1195,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         part[D * kTreeRows] = mm;
         part[(D + 1) * kTreeRows] = ll;
       }
-      // The values of drafts were looked at; weights of 0 (a copy's for the keys
-      // of the others, a factor's) turn an infinity of the context into a NaN.
-      // Where either shows, the sum of the non-finite values that the row sees
-      // in this segment is the result (a NaN of the scores is one anyway).
-      auto mend = [&](int c, float (&o)[8]) {
-        float sum[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-        const int to = (int)min((long long)x.len, (long long)x.t1 * NT);
-#pragma unroll 1
-        for (int pos = x.t0 * NT; pos < to; ++pos) {
-          const int a = pos - x.base;
-          if (a >= 0 && !(anc[a >> 5] >> (a & 31) & 1u)) continue;
-          const int id = __ldg(p.block_tables + (size_t)x.seq * p.c.max_blocks + pos / kPageTokens);
-          if (id < 0 || id >= p.c.num_blocks) continue;
-          const uint16_t* v = static_cast<const uint16_t*>(p.c.v_cache) +
-                              (((size_t)id * p.c.num_kv_heads + x.g) * D + c) * kPageTokens +
-                              pos % kPageTokens;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint16_t e = v[i * kPageTokens];
-            if ((e & Half16<T>::kExp) == Half16<T>::kExp) sum[i] += Half16<T>::widen(e);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (!(sum[i] - sum[i] == 0.f)) o[i] = sum[i];
-      };
+      // Output steps (a bit each) that are not finite, to be mended at the end
+      uint32_t wild = 0;
       tc_fence_after();
 #pragma unroll 1
       for (int c = grp * (D / NG); c < (grp + 1) * (D / NG); c += kStageCols) {
@@ -1163,15 +1239,12 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           softmax_barrier(2 + grp, 128);
         }
         if (r >= rows || !ok) continue;
-        float wild[4] = {0.f, 0.f, 0.f, 0.f};
+        float apart[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kStageCols; ++i)
-          if (i < width) wild[i % 4] += o[i] - o[i];
-        if (!nan && (odd || !((wild[0] + wild[1]) + (wild[2] + wild[3]) == 0.f))) {
-#pragma unroll
-          for (int i = 0; i < kStageCols; i += 8)
-            if (i < width) mend(c0 + i, *reinterpret_cast<float(*)[8]>(o + i));
-        }
+          if (i < width) apart[i % 4] += o[i] - o[i];
+        if (!((apart[0] + apart[1]) + (apart[2] + apart[3]) == 0.f))
+          wild |= 1u << ((c - grp * (D / NG)) / kStageCols);
         if (!whole) {
 #pragma unroll
           for (int i = 0; i < kStageCols; ++i)
@@ -1189,6 +1262,18 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       }
       __syncwarp();
       tc_fence_before();
+      // The values of drafts were looked at; weights of 0 (a copy's for the keys
+      // of the others, a factor's) turn an infinity of the context into a NaN.
+      // Where either shows, the sum of the non-finite values that the row sees
+      // in this segment is the result (a NaN of the scores is one anyway).
+      const bool branch = odd && r < rows && ok && !nan;
+      if (nan) wild = 0;
+      if (__any_sync(0xffffffffu, wild != 0 || branch)) {
+        const int width = kStageCols / copies;
+        mend_non_finite<D, T>(p, x.seq, x.g, x.t0 * NT, (int)min((long long)x.len, (long long)x.t1 * NT),
+                              x.base, anc, grp * (D / NG) + copy * width, width, wild, branch, scale,
+                              dst, whole ? nullptr : part);
+      }
       if (drafts) {
         if (lane == 0) mbar_arrive(bar(C::ANC_EMPTY + a2));
         ++uses;
