@@ -7,6 +7,7 @@
 #include <climits>
 #include <cstdint>
 
+#include "packed_slice.h"
 #include "paged_cache_internal.h"
 #include "paged_walk.cuh"
 #include "ptx.cuh"
@@ -27,8 +28,9 @@ __device__ __forceinline__ NewTokens new_tokens(const int32_t* __restrict__ cu,
                                                 const int32_t* __restrict__ seq_lens, int i,
                                                 int total) {
   NewTokens t;
-  t.lo = max(__ldg(cu + i), 0);
-  t.n = max(min(__ldg(cu + i + 1), total) - t.lo, 0);
+  const PackedSlice rows = packed_slice(__ldg(cu + i), __ldg(cu + i + 1), total);
+  t.lo = rows.lo;
+  t.n = rows.n;
   t.len = max(__ldg(seq_lens + i), 0);
   return t;
 }

@@ -79,6 +79,7 @@
 #include <cstdint>
 
 #include "attn_varlen_device.cuh"
+#include "packed_slice.h"
 #include "paged_tree_internal.h"
 #include "paged_walk.cuh"
 #include "ptx.cuh"
@@ -232,8 +233,9 @@ struct SeqInfo {
 template <int D>
 __device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int group, int i) {
   SeqInfo s;
-  s.lo = max(__ldg(p.cu + i), 0);
-  s.n = max(min(__ldg(p.cu + i + 1), p.total_q) - s.lo, 0);
+  const PackedSlice rows = packed_slice(__ldg(p.cu + i), __ldg(p.cu + i + 1), p.total_q);
+  s.lo = rows.lo;
+  s.n = rows.n;
   const int len = max(__ldg(p.seq_lens + i), 0);
   s.base = len - s.n;
   s.len = (int)min((long long)len, (long long)p.c.max_blocks * kPageTokens);
@@ -373,7 +375,7 @@ __device__ __forceinline__ void non_finite_sums(const TreeParams& p, int seq, in
 // whole warp calls; rows without any have wild 0 and branch false.
 //
 // Bound by the latency of its loads.  A CTA that holds three row tiles of 131072
-// tokens each, 6 query heads' rows on one KV head, bf16, takes 5.2 ms at D = 256
+// tokens each (3 drafts, 2 query heads, bf16) takes 5.2 ms at D = 256
 // without such values, 5.2 with some in the drafts, 11.7 with four in the context,
 // 33 with one in every dimension; at D = 128 3.0, 3.0, 5.7 and 8.7.  (Each row
 // reading all positions for itself took 190 ms for 24000 tokens, in which waits
