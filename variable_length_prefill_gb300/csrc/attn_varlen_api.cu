@@ -62,6 +62,10 @@ void* g_noalloc_ptr[kMaxDevices] = {};
 // graph that holds its address stays valid.
 static __device__ int g_page_status;
 int* g_page_status_ptr[kMaxDevices] = {};
+// What a check has taken out of a status word, on its way to the host; checks
+// take turns.
+static __device__ int g_taken;
+std::mutex g_check_mu;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 bool g_encode_probed = false;
 
@@ -339,17 +343,32 @@ int cache_shape(avp::CacheShape& c, void* k_cache, void* v_cache, int num_seqs, 
   return ATTN_VARLEN_OK;
 }
 
-// Read and clear the paged-cache operators' status word (null: they never ran
-// on the device).  The stream has been synchronised.
-int read_and_clear_page_status(int* word) {
+__global__ void take_status_kernel(int* word) { g_taken = atomicExch(word, 0); }
+
+// Read and clear a device's status word behind the work of `stream`.  Kernels of
+// other streams may set bits meanwhile, so what was read is not what there is to
+// clear: one exchange does both.  Nothing is launched where the word is clear.
+int take_status(int* word, cudaStream_t stream, int* status) {
+  *status = 0;
+  cudaError_t e = cudaMemcpyAsync(status, word, sizeof(int), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return fail_cuda(e);
+  if (*status == 0) return ATTN_VARLEN_OK;
+  std::lock_guard<std::mutex> lock(g_check_mu);
+  take_status_kernel<<<1, 1, 0, stream>>>(word);
+  e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = cudaMemcpyFromSymbolAsync(status, g_taken, sizeof(int), 0, cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  return e == cudaSuccess ? ATTN_VARLEN_OK : fail_cuda(e);
+}
+
+// The paged-cache operators' status word (null: they never ran on the device).
+int read_and_clear_page_status(int* word, cudaStream_t stream) {
   if (!word) return ATTN_VARLEN_OK;
   int status = 0;
-  cudaError_t e = cudaMemcpy(&status, word, sizeof(int), cudaMemcpyDeviceToHost);
-  if (e != cudaSuccess) return fail_cuda(e);
-  if (status == 0) return ATTN_VARLEN_OK;
-  const int zero = 0;
-  e = cudaMemcpy(word, &zero, sizeof(int), cudaMemcpyHostToDevice);
-  if (e != cudaSuccess) return fail_cuda(e);
+  const int rc = take_status(word, stream, &status);
+  if (rc || status == 0) return rc;
   if (status & avp::kPageStatusTimeout) return ATTN_VARLEN_ERR_DEVICE_TIMEOUT;
   if (status & avp::kPageStatusBadBlock) return ATTN_VARLEN_ERR_BAD_BLOCK_TABLE;
   if (status & avp::kPageStatusNoBlock) return ATTN_VARLEN_ERR_NO_FREE_BLOCK;
@@ -358,18 +377,11 @@ int read_and_clear_page_status(int* word) {
 }
 
 int read_and_clear_status(void* ws, cudaStream_t stream) {
-  cudaError_t e = cudaStreamSynchronize(stream);
   int status = 0;
-  if (e == cudaSuccess) e = cudaMemcpy(&status, ws, sizeof(int), cudaMemcpyDeviceToHost);
-  if (e != cudaSuccess) return fail_cuda(e);
-  if (status != 0) {
-    const int zero = 0;
-    e = cudaMemcpy(ws, &zero, sizeof(int), cudaMemcpyHostToDevice);
-    if (e != cudaSuccess) return fail_cuda(e);
-    if (status == avp::kPagedStatusBadBlock) return ATTN_VARLEN_ERR_BAD_BLOCK_TABLE;
-    return ATTN_VARLEN_ERR_DEVICE_TIMEOUT;
-  }
-  return ATTN_VARLEN_OK;
+  const int rc = take_status(static_cast<int*>(ws), stream, &status);
+  if (rc || status == 0) return rc;
+  return status == avp::kPagedStatusBadBlock ? ATTN_VARLEN_ERR_BAD_BLOCK_TABLE
+                                             : ATTN_VARLEN_ERR_DEVICE_TIMEOUT;
 }
 
 }  // namespace
@@ -782,7 +794,7 @@ int attn_varlen_check(cudaStream_t stream) {
   }
   rc = ws ? read_and_clear_status(ws, stream) : map_cuda(cudaStreamSynchronize(stream));
   if (rc == ATTN_VARLEN_ERR_CUDA) return rc;
-  const int page_rc = read_and_clear_page_status(word);
+  const int page_rc = read_and_clear_page_status(word, stream);
   return rc ? rc : page_rc;
 }
 
