@@ -289,7 +289,7 @@ def chunk_delta_rule_output(q, k, v, h, g, chunk_size=64, scale=None, out=None, 
 def _torch():
     global _torch_module, _i32, _types, _raw_stream, _device, _take, _give
     import torch
-    _torch_module, _i32, _types = torch, torch.int32, (torch.bfloat16, torch.float16)
+    _i32, _types = torch.int32, (torch.bfloat16, torch.float16)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -299,7 +299,7 @@ def _torch():
         lambda n, stream: torch.cuda.caching_allocator_alloc(n, None, stream))
     _give = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None) or \
         torch.cuda.caching_allocator_delete
-    return torch
+    _torch_module = torch  # last: other threads take it for all of the above
 
 
 _torch_module = _i32 = _types = _raw_stream = _device = _take = _give = None
