@@ -795,7 +795,7 @@ int attn_varlen_check(cudaStream_t stream) {
   rc = ws ? read_and_clear_status(ws, stream) : map_cuda(cudaStreamSynchronize(stream));
   if (rc == ATTN_VARLEN_ERR_CUDA) return rc;
   const int page_rc = read_and_clear_page_status(word, stream);
-  return rc ? rc : page_rc;
+  return rc == ATTN_VARLEN_OK || page_rc == ATTN_VARLEN_ERR_DEVICE_TIMEOUT ? page_rc : rc;
 }
 
 int attn_varlen_check_ws(void* workspace, cudaStream_t stream) {
