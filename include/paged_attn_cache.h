@@ -15,7 +15,8 @@
  * arrays.  Calls are asynchronous on `stream`, read nothing back and allocate
  * nothing.  The index arrays live on the device, so what is wrong in them is
  * found there: the entry is skipped as described, and attn_varlen_check on the
- * same stream reports it.  Such a report stays until a check reads it.
+ * same stream reports it.  Such a report stays until a check reads it.  Calls
+ * may come from several threads; those on one stream act one after the other.
  *
  * A page id outside [0, num_blocks) is never used as an address
  * (ATTN_VARLEN_ERR_BAD_BLOCK_TABLE).  block_size is 16 and head_size 64, 128

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <mutex>
 
 #include "packed_slice.h"
 #include "paged_cache_internal.h"
@@ -599,6 +600,11 @@ cudaError_t launch_behind(void (*kernel)(Params), dim3 grid, int threads, const 
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// A fork and a compaction are a plan and what carries it out: no other call that
+// changes counts, lengths or tables may come between the two on their stream,
+// also from another thread.
+std::mutex g_plan_mu;
+
 }  // namespace
 
 cudaError_t launch_cache_write(const CacheWriteParams& p, cudaStream_t stream) {
@@ -622,11 +628,13 @@ cudaError_t launch_cache_accept(const CacheAcceptParams& p, cudaStream_t stream)
 }
 
 cudaError_t launch_cache_free(const CacheFreeParams& p, cudaStream_t stream) {
+  std::lock_guard<std::mutex> lock(g_plan_mu);
   cache_free_kernel<<<p.num_rows, kFreeThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_fork(const CacheForkParams& p, cudaStream_t stream) {
+  std::lock_guard<std::mutex> lock(g_plan_mu);
   fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -634,6 +642,7 @@ cudaError_t launch_cache_fork(const CacheForkParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_cache_compact(const CacheCompactParams& p, cudaStream_t stream) {
+  std::lock_guard<std::mutex> lock(g_plan_mu);
   compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
