@@ -55,8 +55,9 @@ size_t paged_attn_tree_workspace_size(int head_size);
  *   num_seqs, total_q   >= 0 (either 0: returns ATTN_VARLEN_OK, launches nothing)
  *   scale         > 0 and at most 2^126, or <= 0 for head_size^-1/2
  *   dtype         PAGED_ATTN_BF16 (0) or PAGED_ATTN_FP16 (1)
- *   out           like query, not overlapping the inputs; rows that no
- *                 sequence covers are not written
+ *   out           like query, not overlapping the inputs (over query:
+ *                 ATTN_VARLEN_ERR_INVALID_ARG); rows that no sequence covers
+ *                 are not written
  *   workspace     device buffer of paged_attn_tree_workspace_size(head_size)
  *                 bytes, 16-byte aligned, its contents free; calls that can
  *                 overlap on the GPU need one each

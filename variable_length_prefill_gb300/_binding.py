@@ -548,6 +548,10 @@ def paged_attn_tree(query, k_cache, v_cache, block_tables, seq_lens, cu_seqlens,
             raise ValueError(f"query and out must be contiguous {dtype} tensors [total, Hq, {d}] on "
                              f"CUDA device {dev}")
     total, hq, _ = shape
+    if out is not None:
+        apart = out.data_ptr() - query.data_ptr()
+        if total and abs(apart) < total * hq * d * 2:
+            raise ValueError("out must not overlap query")
     if parents is not None:
         _ints(parents, (total,), dev, "parents")
     if scale is None:

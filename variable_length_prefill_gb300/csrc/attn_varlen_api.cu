@@ -762,6 +762,10 @@ int paged_attn_tree(const void* query, const void* k_cache, const void* v_cache,
   if (!(scale == scale) || scale > 0x1p126f) return ATTN_VARLEN_ERR_INVALID_ARG;
   if (workspace_bytes < paged_attn_tree_workspace_size(head_size))
     return ATTN_VARLEN_ERR_WORKSPACE_SMALL;
+  // row tiles are finished while others, split over CTAs, still read their queries
+  const uintptr_t from = reinterpret_cast<uintptr_t>(query), to = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t bytes = (uintptr_t)total_q * num_query_heads * head_size * 2;
+  if (from < to + bytes && to < from + bytes) return ATTN_VARLEN_ERR_INVALID_ARG;
   avp::TreeParams p;
   if ((rc = cache_shape(p.c, const_cast<void*>(k_cache), const_cast<void*>(v_cache), num_seqs,
                         num_kv_heads, head_size, max_blocks_per_seq, num_blocks)))
