@@ -20,8 +20,9 @@
  *
  * A page id outside [0, num_blocks) is never used as an address
  * (ATTN_VARLEN_ERR_BAD_BLOCK_TABLE).  block_size is 16 and head_size 64, 128
- * or 256, as for paged_attn_decode.  num_seqs == 0 (or no token, row or fork
- * to work on) returns ATTN_VARLEN_OK and launches nothing.
+ * or 256, as for paged_attn_decode.  num_seqs and the number of forks are at
+ * most 2^30 (else ATTN_VARLEN_ERR_INVALID_ARG).  num_seqs == 0 (or no token,
+ * row or fork to work on) returns ATTN_VARLEN_OK and launches nothing.
  */
 #ifndef PAGED_ATTN_CACHE_H_
 #define PAGED_ATTN_CACHE_H_

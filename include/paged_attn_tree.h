@@ -52,7 +52,8 @@ size_t paged_attn_tree_workspace_size(int head_size);
  *   cu_seqlens    int32 device [num_seqs + 1], taken as clipped to [0, total_q];
  *                 a negative slice is empty, slices do not overlap
  *   parents       int32 device [total_q], or null for chains
- *   num_seqs, total_q   >= 0 (either 0: returns ATTN_VARLEN_OK, launches nothing)
+ *   num_seqs, total_q   >= 0, num_seqs at most 2^30 (either 0: returns
+ *                 ATTN_VARLEN_OK, launches nothing)
  *   scale         > 0 and at most 2^126, or <= 0 for head_size^-1/2
  *   dtype         PAGED_ATTN_BF16 (0) or PAGED_ATTN_FP16 (1)
  *   out           like query, not overlapping the inputs (over query:

@@ -296,6 +296,9 @@ int current_device(int* dev) {
   return ATTN_VARLEN_OK;
 }
 
+// Loops over sequences and forks step past their ends in 32 bits.
+constexpr int kMostRows = 1 << 30;
+
 // Checks shared by the paged-cache operators; OK also where there is nothing
 // to do.
 int check_cache(const void* k_cache, const void* v_cache, int num_kv_heads, int head_size,
@@ -583,7 +586,7 @@ int paged_attn_cache_write(const void* key, const void* value, void* k_cache, vo
                            int max_blocks_per_seq, int num_blocks, int64_t key_token_stride,
                            int64_t key_head_stride, int64_t value_token_stride,
                            int64_t value_head_stride, cudaStream_t stream) {
-  if (num_seqs < 0 || total_tokens < 0) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (num_seqs < 0 || num_seqs > kMostRows || total_tokens < 0) return ATTN_VARLEN_ERR_INVALID_ARG;
   if (num_seqs == 0 || total_tokens == 0) return ATTN_VARLEN_OK;
   int rc = check_cache(k_cache, v_cache, num_kv_heads, head_size, block_size, max_blocks_per_seq,
                        num_blocks);
@@ -670,7 +673,8 @@ int paged_attn_cache_fork(void* k_cache, void* v_cache, int32_t* block_tables, i
                           int num_seqs, int num_kv_heads, int head_size, int block_size,
                           int max_blocks_per_seq, int num_blocks, void* workspace,
                           size_t workspace_bytes, cudaStream_t stream) {
-  if (num_forks < 0 || num_seqs < 0) return ATTN_VARLEN_ERR_INVALID_ARG;
+  if (num_forks < 0 || num_forks > kMostRows || num_seqs < 0 || num_seqs > kMostRows)
+    return ATTN_VARLEN_ERR_INVALID_ARG;
   if (num_forks == 0) return ATTN_VARLEN_OK;
   if (num_seqs < 1) return ATTN_VARLEN_ERR_INVALID_ARG;
   int rc = check_cache(k_cache, v_cache, num_kv_heads, head_size, block_size, max_blocks_per_seq,
@@ -742,7 +746,7 @@ int paged_attn_tree(const void* query, const void* k_cache, const void* v_cache,
                     int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out,
                     void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   static_assert(PAGED_ATTN_MAX_DRAFTS == avp::kTreeMaxDrafts, "drafts");
-  if (num_seqs < 0 || total_q < 0 || num_kv_heads < 1 || num_query_heads < 1 ||
+  if (num_seqs < 0 || num_seqs > kMostRows || total_q < 0 || num_kv_heads < 1 || num_query_heads < 1 ||
       num_query_heads % num_kv_heads != 0)
     return ATTN_VARLEN_ERR_INVALID_ARG;
   if (dtype != PAGED_ATTN_BF16 && dtype != PAGED_ATTN_FP16) return ATTN_VARLEN_ERR_INVALID_ARG;
