@@ -121,9 +121,10 @@ size_t paged_attn_cache_fork_workspace_size(int num_forks, int num_seqs);
  * For each j, row dst[j] becomes a copy of row src[j] as it stands before the
  * call: whole pages are shared (their counts go up by one); a last page that
  * holds fewer than 16 tokens is copied, keys and values, into a free page,
- * whose count becomes 1; seq_lens[dst[j]] = seq_lens[src[j]].  Table entries
- * past the pages keep their bytes.  Free pages are taken from the lowest id
- * on, in order of j, so the result is always the same.
+ * whose count becomes 1; seq_lens[dst[j]] = seq_lens[src[j]].  An id that is no
+ * page is copied as it is.  Table entries past the pages keep their bytes.
+ * Free pages are taken from the lowest id on, in order of j, so the result is
+ * always the same.
  *
  * dst[j] has to be an empty row (seq_lens 0: freed, or never used), no src of
  * this call, and named once: of several j with the same dst the first counts.

@@ -364,6 +364,10 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(
       // a row longer than its table has no page past the table to copy
       part = holds && p.seq_lens[s] > 0 && p.seq_lens[s] % kPage != 0 &&
              p.seq_lens[s] < p.c.max_blocks * (long long)kPage;
+      if (part) {  // nor has a last id that is no page
+        const int id = p.block_tables[(size_t)s * p.c.max_blocks + p.seq_lens[s] / kPage];
+        part = id >= 0 && id < p.c.num_blocks;
+      }
     }
     int total;
     const int rank = need + block_exclusive(part ? 1 : 0, total, s_warp);
@@ -427,7 +431,9 @@ __global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(
   const int32_t* from = p.block_tables + (size_t)s * p.c.max_blocks;
   int32_t* to = p.block_tables + (size_t)d * p.c.max_blocks;
   const int full = min(len / kPage, p.c.max_blocks);
-  for (int i = part * kForkThreads + threadIdx.x; i < full; i += kForkParts * kForkThreads) {
+  // a last page without a fresh one in its place is a bad id, which is copied
+  const int ids = fresh >= 0 ? full : (int)min((len + kPage - 1LL) / kPage, (long long)p.c.max_blocks);
+  for (int i = part * kForkThreads + threadIdx.x; i < ids; i += kForkParts * kForkThreads) {
     const int id = from[i];
     to[i] = id;
     if (id < 0 || id >= p.c.num_blocks)
@@ -444,10 +450,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(
   }
   if (fresh < 0) return;
   const int last = from[full];
-  if (last < 0 || last >= p.c.num_blocks) {
-    if (threadIdx.x == 0) atomicOr(p.c.status, kPageStatusBadBlock);
-    return;
-  }
+  if (last < 0 || last >= p.c.num_blocks) return;  // only if the table changed under the kernel
   const int page = p.c.num_kv_heads * p.c.head_size * 2;  // 16-byte pieces
   const int a = (int)((long long)page * part / kForkParts);
   const int b = (int)((long long)page * (part + 1) / kForkParts);
