@@ -1091,8 +1091,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           const float ms = m * p.scale_log2;
           float mul = p.scale_log2, off = Half16<T>::kWeightLog2 - ms;
           if (!(fabsf(ms) < 0x1p23f)) {
-            const int e = min(__float_as_int(p.scale_log2) >> 23,
-                              127 + 227 - (__float_as_int(m) >> 23 & 255));
+            const int e = max(1, min(__float_as_int(p.scale_log2) >> 23,
+                                     127 + 227 - (__float_as_int(m) >> 23 & 255)));
             mul = __int_as_float(e << 23);
             off = m == -INFINITY ? 0.f : __fadd_rd(Half16<T>::kWeightLog2, -(m * mul));
           }
