@@ -180,9 +180,12 @@ __global__ void __launch_bounds__(kWriteThreads, 4) cache_write_kernel(
 // stores: threads never touch one another's elements, so no barrier is needed
 // between moves.
 //
-// Bound by the value cache's 32-byte sectors, of which a move uses 2 bytes
-// each: 256 sequences, up to 12 of 64 drafts, 8 heads of 128, 14.5 us for 50 MB
-// of sectors read and as much written (13 MB of keys and values in all).  4 sequences, up to 4 of 8: 3.2 us.
+// Bound by the form of the work, not by a memory: 256 sequences, up to 12 of 64
+// drafts, 8 heads of 128 take 14.5 us with DRAM at a fifth.  A value moves as 2
+// bytes of a sector of its own, 44 MB of sectors touched each way, of which 17
+// MB read and 10 MB written are distinct (5 us with the keys at a copy's
+// bandwidth), by up to two batches of loads and stores that wait for each other.
+// 4 sequences, up to 4 of 8: 3.2 us.
 constexpr int kAcceptThreads = 128;
 constexpr int kAcceptBatch = 128;  // moves resolved through the table at a time
 

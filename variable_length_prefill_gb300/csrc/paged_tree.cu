@@ -65,10 +65,11 @@
 //
 // Measured (both kernels of a call, captured; 32 query and 8 KV heads, D = 128
 // unless said): 64 x 4096 tokens, 16 drafts 186 us, 5.9 TB/s, 87 % of a copy's
-// bandwidth (D = 64: 113 us, 71 %).  3 sequences of up to 131071, 33 drafts, 40
-// query heads 216 us, 5.3 TB/s: tiles of 128 rows take about 2000 clocks,
-// scores, softmax and value product one behind the other, tensor pipe 40 % busy.
-// 16 of up to 2112, 64 drafts, 4 KV heads, D = 256 49.5 us, tensor pipe 25 %
+// bandwidth (D = 64: 113 us, 71 %: the issue of 2 KB copies); one token each 179
+// us (D = 64: 101).  3 sequences of up to 131071, 33 drafts, 40 query heads 216
+// us, 5.3 TB/s: tiles of 128 rows take about 2000 clocks, scores, softmax and
+// value product one behind the other, tensor pipe 40 % busy.
+// 16 of up to 2112, 64 drafts, 4 KV heads, D = 256 50 us, tensor pipe 25 %
 // busy: 1800 clocks a 64-key tile (1060 of products) and 20000 for a row tile's
 // start and end.  4 x 128 tokens, 8 drafts 12.9 us, all latency.
 #include <cuda_bf16.h>
@@ -122,18 +123,20 @@ struct TreeCfg {
   static constexpr int SOFTMAX = 128 * NG;  // softmax threads
   // A row tile's fixed cost (query rows in, filling the pipeline, output) in key
   // tiles, for the CTAs' equal shares.  Counted as 5 / 7 / 8 / 10 tiles, 16
-  // sequences of up to 2112 tokens and 64 drafts at D = 256 took 51.8 / 47.7 /
-  // 48.4 / 48.2 us; counted as 3 / 4 / 5 / 6, at D = 128 with 8 KV heads 47.8 /
-  // 41.2 / 43.2 / 40.9, and 5 of up to 3239 with one KV head 16.5 / 16.5 / 16.3 /
-  // 19.1 (64 x 4096 tokens: no difference).
+  // ragged sequences of up to 2112 tokens and 64 drafts, 32 query and 4 KV heads
+  // of 256, fp16, took 51.8 / 47.7 / 48.4 / 48.2 us; counted as 3 / 4 / 5 / 6, the
+  // same with 8 KV heads of 128, bf16, 47.8 / 41.2 / 43.2 / 40.9, and 5 of up to
+  // 3239 tokens and 20 drafts, 8 query heads on one of 128, bf16, 16.5 / 16.5 /
+  // 16.3 / 19.1 (64 x 4096 tokens: no difference).
   static constexpr int OVERHEAD = D == 256 ? 8 : 4;
   // No share is smaller than this, nor than least(): more CTAs on a row tile
-  // leave more partial results to join.  At D = 128 a first turn (4 x 128 tokens)
-  // took 12.6 us with 2 and 13.0 with 4, 5 x 3239 tokens 16.5 and 17.8.
+  // leave more partial results to join.  At D = 128 a first turn (4 x 128 tokens,
+  // 8 drafts, 32 query and 8 KV heads, fp16) took 12.6 us with 2 and 13.0 with 4,
+  // the 5 of up to 3239 tokens 16.5 and 17.8.
   static constexpr int LEAST = D == 256 ? 4 : 2;
   // s units a share take time as s, and the parts of a row tile of m units as
-  // m / s, least together at s ~ sqrt(m).  One token on 20000 / 100000 at D = 64:
-  // 16.9 / 27.6 us with m / 5 under the root, 17.0 / 26.3 with m / 10, 18.3 /
+  // m / s, least together at s ~ sqrt(m).  One token on 20000 / 100000, 8 query
+  // heads on one of 64, bf16: 16.9 / 27.6 us with m / 5 under the root, 17.0 / 26.3 with m / 10, 18.3 /
   // 25.7 with m / 20, 16.6 / 34 with 4 units for both.
   __device__ static int least(int longest) {
     return max(LEAST, (int)sqrtf(0.1f * (float)longest));
