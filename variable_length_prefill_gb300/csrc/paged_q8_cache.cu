@@ -144,6 +144,17 @@ __device__ __forceinline__ void store_words(void* dst, const uint32_t* w) {
   }
 }
 
+// 32 bytes of a sector, in one store where they begin one (a cache's base may be 16 bytes
+// past: then in two).
+__device__ __forceinline__ void store_sector(uint8_t* dst, const uint32_t (&w)[8]) {
+  if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  else
+    store_words<8>(dst, w);
+}
+
 // --------------------------------------------------------------------- write
 // The larger magnitudes of two pairs; NaN wins.
 template <bool FP16>
@@ -361,9 +372,7 @@ __device__ __forceinline__ void write_page(const PageTask& k, const uint16_t* sr
           o[4 * h + j] = float_to_codes<INT8>(f[0], f[1], f[2], f[3]);
         }
       if constexpr (FULL) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + e * kPage), "r"(o[0]),
-                     "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                     : "memory");
+        store_sector(dst + e * kPage, o);
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
