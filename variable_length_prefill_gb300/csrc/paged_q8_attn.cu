@@ -471,16 +471,13 @@ __device__ __forceinline__ void take_pages(const uint32_t (&slot)[NP], const uin
         f[i][e] = f[i][e] > 0x1p90f ? 0x1p90f : f[i][e];
       }
     auto unseen = [&](int i, int e) { return MASKED && !(seen[i] >> (4 * nt + e) & 1); };
-    auto scores = [&] {
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
+    for (int i = 0; i < NP; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          d[i][e] = fmaf(s[i][nt][e], f[i][e & 1], -w.m[nt][e & 1]);
-          if (unseen(i, e)) d[i][e] = -INFINITY;
-        }
-    };
-    scores();
+      for (int e = 0; e < 4; ++e) {
+        d[i][e] = fmaf(s[i][nt][e], f[i][e & 1], -w.m[nt][e & 1]);
+        if (unseen(i, e)) d[i][e] = -INFINITY;
+      }
     // A maximum may be passed by kSlack before anything is rescaled, so that the
     // lanes need not agree on one for every page.
     bool up = false;
@@ -516,7 +513,13 @@ __device__ __forceinline__ void take_pages(const uint32_t (&slot)[NP], const uin
         w.m[nt][e] = m;
         w.x[nt][e] = x;
       }
-      scores();
+      // From rounded products, as the maxima are: what the product's rounding cuts from
+      // a score, half its last bit, passes any slack from 2^27 on.
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          d[i][e] = unseen(i, e) ? -INFINITY : __fmul_rn(s[i][nt][e], f[i][e & 1]) - w.m[nt][e & 1];
     }
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
