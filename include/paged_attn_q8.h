@@ -134,7 +134,9 @@ size_t paged_attn_q8_workspace_size(int head_size);
  * 2^-31 of its largest and within 2^-39 of the largest otherwise.  Weights, with
  * the page's scale of the values, are rounded to fp16 for the value product
  * (products of weight and scale below 2^-32 of the row's largest may count as
- * 0), and the output once.
+ * 0), and the output once.  Queries, scale and key scales may be of any size in
+ * their ranges, whether or not they make up for each other; scores that, times
+ * log2 e, pass 2^100 are told apart to 2^-19 of themselves.
  *
  *   query, out    device [total_q, num_query_heads, head_size] of dtype, 16-byte
  *                 aligned, not overlapping (else ATTN_VARLEN_ERR_INVALID_ARG);

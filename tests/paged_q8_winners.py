@@ -4,12 +4,12 @@ import numpy as np
 import paged_q8_ref as ref
 
 
-def winners(q, cache, tables, lens, cu, kind, scale, most=np.inf):
+def winners(q, cache, tables, lens, cu, kind, scale, fold=0.0):
     """(out, decided): the value of the key with the largest score, and whether its lead is sure.
 
-    Scores times log2 e past `most` in magnitude count as `most`.  A score is off by (d + 8) 2^-23 of the sum
-    of its products' magnitudes (sums in 32 bits, which tensor cores may cut) and by 4 roundings of 2^-24 of
-    itself; a lead of 400 more than twice that leaves the others no weight, whatever the size of their values."""
+    A score is off by (d + 8) 2^-23 of the sum of its products' magnitudes (sums in 32 bits, which tensor
+    cores may cut), by 4 roundings of 2^-24 of itself and by `fold` of itself, for what is told apart no further;
+    a lead of 400 more than twice that leaves the others no weight, whatever the size of their values."""
     k, v, ks, vs = cache
     total, hq, d = q.shape
     group = hq // v.shape[1]
@@ -21,8 +21,8 @@ def winners(q, cache, tables, lens, cu, kind, scale, most=np.inf):
             for h in range(hq if seen.size else 0):
                 a, x = key[seen, h // group], q[lo + j, h]
                 to_log2 = scale * np.log2(np.e)
-                s = np.clip((a @ x) * to_log2, -most, most)
-                off = (d + 8) * 2.0 ** -23 * (np.abs(a) @ np.abs(x)).max() * to_log2 + 4 * 2.0 ** -24 * np.abs(s).max()
+                s = a @ x * to_log2
+                off = (d + 8) * 2.0 ** -23 * (np.abs(a) @ np.abs(x)).max() * to_log2 + (4 * 2.0 ** -24 + fold) * np.abs(s).max()
                 best = int(s.argmax())
                 rest = np.delete(s, best)
                 decided[lo + j, h] = not rest.size or s[best] - rest.max() > 2 * off + 400

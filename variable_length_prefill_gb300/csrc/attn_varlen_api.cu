@@ -938,6 +938,7 @@ int paged_attn_q8(const void* query, const void* k_cache, const void* v_cache,
   p.group = num_query_heads / num_kv_heads;
   const double s = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)head_size);
   p.scale_log2 = (float)(1.4426950408889634 * s);
+  p.scale_frac = (float)std::frexp(1.4426950408889634 * s, &p.scale_exp);
   p.fp16 = dtype == PAGED_ATTN_FP16;
   p.test_withhold = g_test_withhold;
   return map_cuda(avp::launch_q8_attn(p, code == PAGED_ATTN_Q8_INT8, stream));

@@ -71,6 +71,11 @@ constexpr float kNone = -3.0e38f;    // maximum of a row that has seen nothing
 constexpr float kLeast = -200.f;     // least exponent of O (scales are 2^-149 at least)
 constexpr float kSlack = 6.f;        // a maximum may be passed by this much before O is rescaled
 constexpr float kBase = 8.f;         // weights are held 2^8 times as large: 2^14 at most
+// Rows up to kMostRow (a query's power of two) under a softmax scale (times log2 e) up to
+// kMostScale have all scores of a page below 2^125 if its key scale is up to
+// kMostKeyScale: products of fp16 and codes are below 2^33.  What is past one of the three
+// may still be an ordinary score; it takes the way of settle_scores.
+constexpr float kMostRow = 0x1p16f, kMostScale = 0x1p30f, kMostKeyScale = 0x1p46f;
 // What a row tile costs beside its pages, in pages, and a warp's range at least, in pages
 // and kPartCost: 3 and 6 are the best of (1 to 4, 4 to 12) over contexts of 400 to 4096
 // (2, 4: 10 % slower on 16 x 8 drafts of head size 256; 3, 8: 10 % on 2 x 4096).
@@ -189,6 +194,8 @@ __device__ __forceinline__ float nan_f() { return __uint_as_float(0x7fffffffu); 
 __device__ __forceinline__ float valid_scale(float s) {
   return s >= 0.f && s <= 3.402823466e38f ? s : nan_f();
 }
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // x 2^e for e in [-400, 400], without a factor that leaves 32 bits
 __device__ __forceinline__ float times_exp2(float x, float e) {
   const float h = exp2f(0.5f * e);
@@ -301,7 +308,8 @@ struct Rows {
   static constexpr bool KEPT = Cfg<D, NT>::KEPT;
   uint32_t kept[KEPT ? NT : 1][D / 16][2];  // query rows as operands
   uint4* lane_q;                            // or where this lane has them: two operands' worth each
-  float qf[NT][2];            // what a product has to be scaled by, rows 2 t, 2 t + 1
+  float qf[NT][2];            // powers of two that the operands were divided by, rows 2 t, 2 t + 1
+  float most;                 // key scales up to this leave all scores below 2^125
   float m[NT][2], x[NT][2], l[NT][2];
   float o[NT][D / 16][4];
 };
@@ -313,6 +321,7 @@ __device__ __forceinline__ void load_rows(const Q8AttnParams& p, const Part& par
                                           Rows<D, NT, INT8>& w) {
   const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   const uint32_t inf = p.fp16 ? 0x7c00u : 0x7f80u;
+  bool large = p.scale_log2 > kMostScale;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int row = part.tile * (8 * NT) + nt * 8 + r, j = row / group;
@@ -359,10 +368,7 @@ __device__ __forceinline__ void load_rows(const Q8AttnParams& p, const Part& par
         w.lane_q[(k * NT + nt) * 32] = make_uint4(q[2 * k][0], q[2 * k][1], q[2 * k + 1][0], q[2 * k + 1][1]);
     }
     __syncwarp();
-    // past 2^50 scores are so far apart that the largest has all the weight (or
-    // shares it with its equals), as it has with the cut factor
-    qf *= p.scale_log2;
-    qf = qf > 0x1p50f ? 0x1p50f : qf;
+    large |= qf > kMostRow;
     w.qf[nt][0] = __shfl_sync(0xffffffffu, qf, t * 8);
     w.qf[nt][1] = __shfl_sync(0xffffffffu, qf, t * 8 + 4);
 #pragma unroll
@@ -371,6 +377,47 @@ __device__ __forceinline__ void load_rows(const Q8AttnParams& p, const Part& par
     for (int k = 0; k < D / 16; ++k)
 #pragma unroll
       for (int e = 0; e < 4; ++e) w.o[nt][k][e] = 0.f;
+  }
+  w.most = __any_sync(0xffffffffu, large) ? -1.f : kMostKeyScale;
+}
+
+// x >= 0 (or NaN) as m 2^e with m below 4, added to e.
+__device__ __forceinline__ float split(float x, int& e) {
+  if (x < 0x1p-126f) x *= 0x1p24f, e -= 24;
+  const int k = min(max((int)(__float_as_uint(x) >> 23) - 127, -126), 126);
+  e += k;
+  return x * power_of_two(-k);
+}
+
+// The scores of a page's products for two rows, where the row's power of two, the softmax
+// scale and the key scale may be any: their exponents meet as integers, so that none is
+// cut or lost before the others make up for it.  Scores past 2^kLinear in magnitude, of
+// which the largest has all the weight, are folded, sixteen powers of two into one: 32 bits
+// hold the order of all there can be (2^407), to 2^-19 of a score.  Beside the other
+// pages' way this code costs 256 short contexts 7 % (19.4 us against 18.0 without it),
+// four contexts of 128 and batches of 4096 nothing.
+constexpr int kLinear = 100;
+
+__device__ __forceinline__ void settle_scores(const Q8AttnParams& p, float ks, const float (&qf)[2], const float (&s)[4],
+                                              float (&t)[4]) {
+  constexpr uint32_t kBorder = (uint32_t)(kLinear + 127) << 23;
+  int from = p.scale_exp - 127;
+  const float frac = split(ks, from) * p.scale_frac;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    // in two steps: neither leaves 32 bits unless the score does.  A product is 0 or from
+    // 2^-33 (fp16 times codes) to 2^33, so exponents past 240 say as much as 240
+    const int exp = max(from + (int)(__float_as_uint(qf[e]) >> 23), -240), near = min(exp, 240);
+    const float half = power_of_two(near >> 1), rest = power_of_two(near - (near >> 1));
+    const float m = frac + (qf[e] - qf[e]);  // NaN stays
+#pragma unroll
+    for (int h = e; h < 4; h += 2) {
+      const float x = s[h] * m, y = x * half * rest;
+      // x 2^exp as bits of a number with a wider exponent, past the border's
+      const uint32_t past = (__float_as_uint(x) & 0x7fffffffu) + ((uint32_t)exp << 23) - kBorder;
+      const uint32_t folded = (kBorder + (past >> 4)) | (__float_as_uint(x) & 0x80000000u);
+      t[h] = fabsf(y) >= __uint_as_float(kBorder) ? __uint_as_float(folded) : y;
+    }
   }
 }
 
@@ -391,8 +438,9 @@ __device__ __forceinline__ int token_of(int r, int upper) {
 // page, page + 1, ...
 // MASKED: not every row sees every token of them.
 template <bool MASKED, int NP, int D, int NT, bool INT8>
-__device__ __forceinline__ void take_pages(const uint32_t (&slot)[NP], const uint32_t (&meta)[NP], int page,
-                                           const Part& part, int group, Rows<D, NT, INT8>& w) {
+__device__ __forceinline__ void take_pages(const Q8AttnParams& p, const uint32_t (&slot)[NP],
+                                           const uint32_t (&meta)[NP], int page, const Part& part, int group,
+                                           Rows<D, NT, INT8>& w) {
   const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   // the products of a page's dimensions in two sums where little else is in flight
   constexpr int CHAINS = NP * NT == 1 ? 2 : 1;
@@ -434,10 +482,13 @@ __device__ __forceinline__ void take_pages(const uint32_t (&slot)[NP], const uin
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[0][0][e] += s2[0][0][e];
   }
-  float ks[NP], lv[NP];
+  float ks[NP], lv[NP];  // the keys' scale times the softmax's
+  bool extreme = false;  // factors or scores may leave 32 bits
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    ks[i] = valid_scale(lds_float(meta[i]));
+    const float k = valid_scale(lds_float(meta[i]));
+    extreme |= k > w.most;
+    ks[i] = k * p.scale_log2;
     lv[i] = __log2f(valid_scale(lds_float(meta[i] + 4)));
   }
   uint32_t seen[NP];  // bit 4 nt + e: that score counts
@@ -462,14 +513,10 @@ __device__ __forceinline__ void take_pages(const uint32_t (&slot)[NP], const uin
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float f[NP][2], d[NP][4];
-    // only a scale past 2^40 could take a finite product out of 32 bits
 #pragma unroll
     for (int i = 0; i < NP; ++i)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        f[i][e] = ks[i] * w.qf[nt][e];
-        f[i][e] = f[i][e] > 0x1p90f ? 0x1p90f : f[i][e];
-      }
+      for (int e = 0; e < 2; ++e) f[i][e] = ks[i] * w.qf[nt][e];
     auto unseen = [&](int i, int e) { return MASKED && !(seen[i] >> (4 * nt + e) & 1); };
 #pragma unroll
     for (int i = 0; i < NP; ++i)
@@ -480,7 +527,7 @@ __device__ __forceinline__ void take_pages(const uint32_t (&slot)[NP], const uin
       }
     // A maximum may be passed by kSlack before anything is rescaled, so that the
     // lanes need not agree on one for every page.
-    bool up = false;
+    bool up = extreme;
 #pragma unroll
     for (int i = 0; i < NP; ++i)
 #pragma unroll
@@ -489,14 +536,25 @@ __device__ __forceinline__ void take_pages(const uint32_t (&slot)[NP], const uin
         up |= over > kSlack || over + lv[i] > w.x[nt][e] + kSlack;
       }
     if (__any_sync(0xffffffffu, up)) {
+      // The scores as rounded products, as the maxima are: what the rounding cuts, half
+      // a last bit, passes any slack from 2^27 on.
+      float t[NP][4];
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[i][e] = __fmul_rn(s[i][nt][e], f[i][e & 1]);
+      if (extreme) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) settle_scores(p, valid_scale(lds_float(meta[i])), w.qf[nt], s[i][nt], t[i]);
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         // of the scores themselves: they may vanish beside the first maximum, kNone
         float top[NP], m = w.m[nt][e];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const float a = unseen(i, e) ? -INFINITY : s[i][nt][e] * f[i][e];
-          const float b = unseen(i, e + 2) ? -INFINITY : s[i][nt][e + 2] * f[i][e];
+          const float a = unseen(i, e) ? -INFINITY : t[i][e];
+          const float b = unseen(i, e + 2) ? -INFINITY : t[i][e + 2];
           top[i] = fmaxf(a, b);
 #pragma unroll
           for (int h = 4; h < 32; h <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], h));
@@ -513,13 +571,11 @@ __device__ __forceinline__ void take_pages(const uint32_t (&slot)[NP], const uin
         w.m[nt][e] = m;
         w.x[nt][e] = x;
       }
-      // From rounded products, as the maxima are: what the product's rounding cuts from
-      // a score, half its last bit, passes any slack from 2^27 on.
 #pragma unroll
       for (int i = 0; i < NP; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          d[i][e] = unseen(i, e) ? -INFINITY : __fmul_rn(s[i][nt][e], f[i][e & 1]) - w.m[nt][e & 1];
+          d[i][e] = unseen(i, e) ? -INFINITY : t[i][e] - w.m[nt][e & 1];
     }
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
@@ -1103,13 +1159,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
 #pragma unroll
       for (int i = 0; i < C::PAGES; ++i) all = all && there[i];
       if (all && (page + C::PAGES) * kPage <= part.all) {
-        take_pages<false, C::PAGES, D, NT, INT8>(slots, meta, page, part, group, w);
+        take_pages<false, C::PAGES, D, NT, INT8>(p, slots, meta, page, part, group, w);
       } else {
 #pragma unroll 1
         for (int i = 0; i < C::PAGES; ++i) {
           const uint32_t one_slot[1] = {slots[0] + i * C::SLOT}, one_meta[1] = {meta[0] + 16 * i};
           if (i == 0 ? there[0] : there[C::PAGES - 1])
-            take_pages<true, 1, D, NT, INT8>(one_slot, one_meta, page + i, part, group, w);
+            take_pages<true, 1, D, NT, INT8>(p, one_slot, one_meta, page + i, part, group, w);
         }
       }
       fence_proxy_async_smem();  // the stage is read before copies write it again

@@ -39,6 +39,8 @@ struct Q8AttnParams {
   int num_query_heads;
   int group;         // query heads of a KV head
   float scale_log2;  // scale * log2(e)
+  float scale_frac;  // the same as scale_frac * 2^scale_exp, scale_frac in [0.5, 1)
+  int scale_exp;
   bool fp16;         // query and out, else bf16
   int test_withhold; // read only by test builds (ATTN_VARLEN_TEST_HOOKS); 0 otherwise
 };
