@@ -96,3 +96,18 @@ def test_equal_scores_past_32_bits_share_the_weight(cuda_lib):
         # six bits, held in eight, round away
         assert (got == want[None]).all()
     cuda_lib.check()
+
+
+@pytest.mark.parametrize("of_q,of_scale,low,high", [(29, 29, 45, 60), (24, 19, 36, 70), (0, 29, 45, 90), (29, 0, 45, 100),
+                                                    (24, 20, 35, 37), (30, 29, 46, 47), (-30, 29, 46, 126)])
+@pytest.mark.parametrize("width", [23, 300])
+def test_pages_on_both_sides_of_large(cuda_lib, width, of_q, of_scale, low, high):
+    """Pages of key scales that are just not large beside such that are, under rows and softmax scales of both kinds."""
+    rng, lens, cu, tables, cache, q = inputs("int8", width)
+    cache[2][:] = np.where(rng.random(cache[2].shape) < 0.5, 2.0 ** low, 2.0 ** high)
+    q = dev(np.clip(q, -1.9, 1.9) * 2.0 ** of_q, torch.bfloat16)
+    got = cuda_lib.paged_attn_q8(q, *upload(cache, "int8"), dev(tables), dev(lens), dev(cu), 2.0 ** of_scale)
+    cuda_lib.check()
+    want, decided = winners(wide(q), cache, tables, lens, cu, "int8", 2.0 ** of_scale, fold=2.0 ** -18)
+    assert decided.mean() > 0.9
+    check_winners(wide(got), want, decided, HALF["bf16"], LEAST["bf16"])

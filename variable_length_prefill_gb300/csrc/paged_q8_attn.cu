@@ -72,10 +72,11 @@ constexpr float kLeast = -200.f;     // least exponent of O (scales are 2^-149 a
 constexpr float kSlack = 6.f;        // a maximum may be passed by this much before O is rescaled
 constexpr float kBase = 8.f;         // weights are held 2^8 times as large: 2^14 at most
 // Rows up to kMostRow (a query's power of two) under a softmax scale (times log2 e) up to
-// kMostScale have all scores of a page below 2^125 if its key scale is up to
+// kMostScale have all scores of a page below 2^kLinear if its key scale is up to
 // kMostKeyScale: products of fp16 and codes are below 2^33.  What is past one of the three
 // may still be an ordinary score; it takes the way of settle_scores.
-constexpr float kMostRow = 0x1p16f, kMostScale = 0x1p30f, kMostKeyScale = 0x1p46f;
+constexpr int kLinear = 100;
+constexpr float kMostRow = 0x1p10f, kMostScale = 0x1p20f, kMostKeyScale = 0x1p36f;
 // What a row tile costs beside its pages, in pages, and a warp's range at least, in pages
 // and kPartCost: 3 and 6 are the best of (1 to 4, 4 to 12) over contexts of 400 to 4096
 // (2, 4: 10 % slower on 16 x 8 drafts of head size 256; 3, 8: 10 % on 2 x 4096).
@@ -309,7 +310,7 @@ struct Rows {
   uint32_t kept[KEPT ? NT : 1][D / 16][2];  // query rows as operands
   uint4* lane_q;                            // or where this lane has them: two operands' worth each
   float qf[NT][2];            // powers of two that the operands were divided by, rows 2 t, 2 t + 1
-  float most;                 // key scales up to this leave all scores below 2^125
+  float most;                 // key scales up to this leave all scores below 2^kLinear
   float m[NT][2], x[NT][2], l[NT][2];
   float o[NT][D / 16][4];
 };
@@ -396,8 +397,6 @@ __device__ __forceinline__ float split(float x, int& e) {
 // hold the order of all there can be (2^407), to 2^-19 of a score.  Beside the other
 // pages' way this code costs 256 short contexts 7 % (19.4 us against 18.0 without it),
 // four contexts of 128 and batches of 4096 nothing.
-constexpr int kLinear = 100;
-
 __device__ __forceinline__ void settle_scores(const Q8AttnParams& p, float ks, const float (&qf)[2], const float (&s)[4],
                                               float (&t)[4]) {
   constexpr uint32_t kBorder = (uint32_t)(kLinear + 127) << 23;
