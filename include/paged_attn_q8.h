@@ -74,7 +74,8 @@ extern "C" {
  * A token whose position is negative is not written; nor is one at or past
  * max_blocks_per_seq * 16 (ATTN_VARLEN_ERR_BAD_BLOCK_TABLE).  Codes of slots
  * past a page's new tokens keep their bytes, as do other pages.  Pages that are
- * written are not shared between rows.
+ * written are not shared between rows; k_cache and v_cache, and k_scale and
+ * v_scale, share no memory (else ATTN_VARLEN_ERR_INVALID_ARG).
  */
 int paged_attn_cache_write_q8(const void* key, const void* value, void* k_cache, void* v_cache,
                               float* k_scale, float* v_scale, const int32_t* block_tables,

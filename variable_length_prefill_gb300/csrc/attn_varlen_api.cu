@@ -804,6 +804,12 @@ bool rows_apart(int64_t tokens, int64_t heads, int64_t size, int64_t token, int6
          (token >= size && head >= (tokens - 1) * token + size);
 }
 
+// Whether two buffers of `bytes` bytes share any.
+bool buffers_meet(const void* a, const void* b, uintptr_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bytes && y < x + bytes;
+}
+
 // Both directions of an 8-bit cache: their arguments differ in what is const.
 int move_q8(const void* key, const void* value, const void* k_cache, const void* v_cache,
             const float* k_scale, const float* v_scale, const int32_t* block_tables,
@@ -830,6 +836,11 @@ int move_q8(const void* key, const void* value, const void* k_cache, const void*
   if (!write &&
       !(rows_apart(total_tokens, num_kv_heads, head_size, key_token_stride, key_head_stride) &&
         rows_apart(total_tokens, num_kv_heads, head_size, value_token_stride, value_head_stride)))
+    return ATTN_VARLEN_ERR_INVALID_ARG;
+  // a scale that keys and values share would be settled by both at once
+  const uintptr_t pages = (uintptr_t)num_blocks * num_kv_heads;
+  if (write && (buffers_meet(k_scale, v_scale, pages * sizeof(float)) ||
+                buffers_meet(k_cache, v_cache, pages * head_size * block_size)))
     return ATTN_VARLEN_ERR_INVALID_ARG;
   avp::Q8MoveParams p;
   if ((rc = cache_shape(p.c, const_cast<void*>(k_cache), const_cast<void*>(v_cache), num_seqs,
