@@ -95,7 +95,8 @@ int paged_attn_cache_write_q8(const void* key, const void* value, void* k_cache,
  *
  *   key, value   device [total_tokens, num_kv_heads, head_size] of dtype,
  *                strided as for paged_attn_cache_write, without rows or heads
- *                that share memory; not overlapping the inputs.  Rows that no
+ *                that share memory, in either or between the two; not
+ *                overlapping the inputs.  Rows that no
  *                sequence covers, and those of negative positions, of positions
  *                at or past max_blocks_per_seq * 16 (ATTN_VARLEN_ERR_BAD_BLOCK_
  *                TABLE) and of bad pages, are not written

@@ -8,6 +8,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
@@ -804,6 +805,23 @@ bool rows_apart(int64_t tokens, int64_t heads, int64_t size, int64_t token, int6
          (token >= size && head >= (tokens - 1) * token + size);
 }
 
+// Whether two such sets of rows of one layout, `by` elements apart, share memory.
+bool rows_meet(int64_t by, int64_t tokens, int64_t heads, int64_t size, int64_t token, int64_t head) {
+  constexpr int64_t kFar = 1ll << 62;  // a single row's stride says nothing
+  if (tokens == 1) token = kFar;
+  if (heads == 1) head = kFar;
+  const bool heads_inside = token > head;
+  const int64_t outer = heads_inside ? token : head, inner = heads_inside ? head : token;
+  const int64_t outers = heads_inside ? tokens : heads, inners = heads_inside ? heads : tokens;
+  by = std::abs(by);
+  for (int64_t i = by / outer; i <= by / outer + 1 && i < outers; ++i) {
+    const int64_t rest = std::abs(by - i * outer);
+    for (int64_t j = rest / inner; j <= rest / inner + 1 && j < inners; ++j)
+      if (std::abs(rest - j * inner) < size) return true;
+  }
+  return false;
+}
+
 // Whether two buffers of `bytes` bytes share any.
 bool buffers_meet(const void* a, const void* b, uintptr_t bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -836,6 +854,12 @@ int move_q8(const void* key, const void* value, const void* k_cache, const void*
   if (!write &&
       !(rows_apart(total_tokens, num_kv_heads, head_size, key_token_stride, key_head_stride) &&
         rows_apart(total_tokens, num_kv_heads, head_size, value_token_stride, value_head_stride)))
+    return ATTN_VARLEN_ERR_INVALID_ARG;
+  // views of one buffer have one layout; others are compared no further than their beginnings
+  const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(value) - reinterpret_cast<uintptr_t>(key)) / 2;
+  if (!write && (apart == 0 || (key_token_stride == value_token_stride && key_head_stride == value_head_stride &&
+                                rows_meet(apart, total_tokens, num_kv_heads, head_size, key_token_stride,
+                                          key_head_stride))))
     return ATTN_VARLEN_ERR_INVALID_ARG;
   // a scale that keys and values share would be settled by both at once
   const uintptr_t pages = (uintptr_t)num_blocks * num_kv_heads;
