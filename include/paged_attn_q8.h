@@ -58,9 +58,10 @@ extern "C" {
  *
  * the page's scale becomes need, if the sequence has no tokens in the page
  * before the new ones; else the larger of need and its scale so far, rounded up
- * to a power of two.  New elements x become the code nearest to x / scale, ties
+ * to a power of two (to 2^127, the largest there is, from above it).  New elements x become the code nearest to x / scale, ties
  * to even.  Where the scale changed, the codes of the page's earlier tokens are
- * rounded anew: the code nearest to code * (old scale / new scale).
+ * rounded anew: the code nearest to code * (old scale / new scale), the largest
+ * code where that is past it (under an old scale above 2^127 only).
  *
  * A non-finite element becomes NaN (e4m3), or -127, 0 or 127 for -infinity, NaN
  * and infinity (integers).  An old scale that is not finite and > 0 counts as
