@@ -53,6 +53,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -1281,8 +1282,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) q8_join_kernel(const __grid_c
 // ------------------------------------------------------------------ launches
 constexpr int kMaxDevices = 64;
 
+// `prepared`, by device, is read by callers of several threads; two may both set the attribute.
 template <class K>
-cudaError_t opt_in(K kernel, int bytes, bool* prepared) {
+cudaError_t opt_in(K kernel, int bytes, std::atomic<bool>* prepared) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1331,14 +1333,14 @@ template <int D, int NT, bool INT8>
 cudaError_t launch_nt(const Q8AttnParams& p, long long rows, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   if (pairs_are_quicker(p, rows, C::ROWS)) {
-    static bool prepared[kMaxDevices] = {};
+    static std::atomic<bool> prepared[kMaxDevices] = {};
     const cudaError_t e = opt_in(q8_attn_kernel<D, NT, INT8, false>, C::BYTES, prepared);
     if (e != cudaSuccess) return e;
     const long long pairs = (long long)p.c.num_seqs * p.c.num_kv_heads;
     const int grid = (int)std::min<long long>(pairs, p.c.sm_count);
     return launch_behind(q8_attn_kernel<D, NT, INT8, false>, dim3(grid), kThreads, C::BYTES, p, stream);
   }
-  static bool prepared[kMaxDevices] = {};
+  static std::atomic<bool> prepared[kMaxDevices] = {};
   cudaError_t e = opt_in(q8_attn_kernel<D, NT, INT8, true>, C::BYTES, prepared);
   if (e != cudaSuccess) return e;
   const int grid = std::min(p.c.sm_count, kQ8MaxSms);

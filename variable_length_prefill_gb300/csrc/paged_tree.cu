@@ -77,6 +77,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "attn_varlen_device.cuh"
@@ -1436,7 +1437,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
 template <int D, typename T>
 cudaError_t launch_dt(const TreeParams& p, cudaStream_t stream) {
   using C = TreeCfg<D>;
-  static bool prepared[kMaxDevices] = {};  // per device: the shared-memory opt-in
+  // per device: the shared-memory opt-in; read by callers of several threads
+  static std::atomic<bool> prepared[kMaxDevices] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
