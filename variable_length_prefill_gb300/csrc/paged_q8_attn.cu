@@ -1297,15 +1297,25 @@ cudaError_t opt_in(K kernel, int bytes, std::atomic<bool>* prepared) {
   return cudaSuccess;
 }
 
-// Whether whole pairs are quicker than ranges, from what the host knows.  A pair's row
-// tiles are one warp's, each about 6 pages' time beside its pages (those of the longest
-// table row); warps go round the pairs, and one sequence may have all the rows that
-// cu_seqlens hands out.  Ranges cost 24 pages' time for two launches and the joins, and
-// 3 a row tile.  A page takes a warp half a microsecond.  Measured: 256 x 16 pairs of up to
-// 4 pages 21 us (ranges: 32), 512 of up to 26 16 us (20), 32 of 9 7.3 us (11); 16 of
-// 257 are split (14 us).
+// Whether whole pairs are quicker than ranges, from what the host knows: counts and the
+// table's width, no lengths.  A pair's row tiles are one warp's, each about 6 pages' time
+// beside its pages (those of the longest table row); warps go round the pairs, and one
+// sequence may have all the rows that cu_seqlens hands out.  Ranges cost 24 pages' time for
+// two launches and the joins, and 3 a row tile.  A page alone takes a warp 0.44 us.
+//
+// Both sides take the table for full, so a context that is much longer than the others
+// would be one warp's alone behind a wide table: kPairPages is where batches of 1 token to
+// the table's width turn.  Measured, one token each, 8 KV heads, pairs | ranges, us: 152
+// contexts of 1 to 1024 tokens 41 | 52, to 1536 59 | 65, to 2048 76 | 73; 304 of them 76 |
+// 80, 110 | 103, 144 | 123; one of 1024, 1536 or 2048 among 151 of 100 32 | 23, 46 | 23, 60 |
+// 23, and one of 65536 1786 | 48.  256 x 16 pairs of up to 4 pages 19 | 31, 64 x 8 of up to 25
+// 15 | 20, 4 x 8 of 9 7.7 | 11; the same behind tables of 64 pages and more, and the first
+// with cu_seqlens, take ranges.
+constexpr int kPairPages = 96;
+
 bool pairs_are_quicker(const Q8AttnParams& p, long long rows, int tile_rows) {
   const long long pairs = (long long)p.c.num_seqs * p.c.num_kv_heads, pages = p.c.max_blocks;
+  if (pages > kPairPages) return false;
   const long long warps = (long long)kTakers * p.c.sm_count;
   const long long tiles = (rows + tile_rows - 1) / tile_rows;  // of a pair, on average
   const long long most = ((p.cu ? (long long)p.total_q : 1) * p.group + tile_rows - 1) / tile_rows;
