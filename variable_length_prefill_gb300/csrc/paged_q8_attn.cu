@@ -305,7 +305,7 @@ struct PairWalk {
 };
 
 // ------------------------------------------------------------------ the kernel
-template <int D, int NT, bool INT8>
+template <int D, int NT>
 struct Rows {
   static constexpr bool KEPT = Cfg<D, NT>::KEPT;
   uint32_t kept[KEPT ? NT : 1][D / 16][2];  // query rows as operands
@@ -318,9 +318,9 @@ struct Rows {
 
 // The tile's query rows: lane (r = lane / 4, t = lane % 4) gets, of row r, dimensions
 // 4 t to 4 t + 3 of each 16, in fp16.
-template <int D, int NT, bool INT8>
+template <int D, int NT>
 __device__ __forceinline__ void load_rows(const Q8AttnParams& p, const Part& part, int group,
-                                          Rows<D, NT, INT8>& w) {
+                                          Rows<D, NT>& w) {
   const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   const uint32_t inf = p.fp16 ? 0x7c00u : 0x7f80u;
   bool large = p.scale_log2 > kMostScale;
@@ -440,7 +440,7 @@ __device__ __forceinline__ int token_of(int r, int upper) {
 template <bool MASKED, int NP, int D, int NT, bool INT8>
 __device__ __forceinline__ void take_pages(const Q8AttnParams& p, const uint32_t (&slot)[NP],
                                            const uint32_t (&meta)[NP], int page, const Part& part, int group,
-                                           Rows<D, NT, INT8>& w) {
+                                           Rows<D, NT>& w) {
   const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   // the products of a page's dimensions in two sums where little else is in flight
   constexpr int CHAINS = NP * NT == 1 ? 2 : 1;
@@ -723,9 +723,9 @@ __device__ __forceinline__ int copy_pages(const Q8AttnParams& p, Walk walk, int 
 }
 
 // A row tile's rows, finished by one warp.
-template <int D, int NT, bool INT8>
+template <int D, int NT>
 __device__ __forceinline__ void write_rows(const Q8AttnParams& p, const Part& part, int group,
-                                           Rows<D, NT, INT8>& w) {
+                                           Rows<D, NT>& w) {
   const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -788,8 +788,8 @@ __device__ __forceinline__ int ring_place(int row, int d) {
 
 // The piece goes to the workspace while the ring is in use, and to the ring (`own`)
 // at the end of the warp's range.
-template <int D, int NT, bool INT8>
-__device__ __forceinline__ void put_piece(const Q8AttnParams& p, int i, Rows<D, NT, INT8>& w,
+template <int D, int NT>
+__device__ __forceinline__ void put_piece(const Q8AttnParams& p, int i, Rows<D, NT>& w,
                                           PieceSums<D, NT>& sums, float* own) {
   const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   float* o = piece_at<D, 8 * NT>(p, blockIdx.x, i) + 4 * 8 * NT;
@@ -1138,11 +1138,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   int taken = 0;        // stages
   bool dead = false;
   Part part;
-  Rows<D, NT, INT8> w;
+  Rows<D, NT> w;
   float* const own = reinterpret_cast<float*>(smem + warp * (C::STAGES * C::STAGE));
   w.lane_q = reinterpret_cast<uint4*>(smem + C::RING) + warp * ((D / 32) * NT * 32) + lane;
   while (!dead && walk.next(p, group, part)) {
-    load_rows<D, NT, INT8>(p, part, group, w);
+    load_rows<D, NT>(p, part, group, w);
     for (int page = part.a; page < part.stop; page += C::PAGES) {
       const uint32_t bar = bars + 16 * stage;
       if (!wait_for(bar, parity, &abort_flag, p.c.status)) {
@@ -1179,10 +1179,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
       const bool ends = part.b == part.s.pages;
       if (part.a > 0) {
         const bool last = walk.left <= 0;
-        put_piece<D, NT, INT8>(p, 2 * warp, w, sums, last ? own : nullptr);
+        put_piece<D, NT>(p, 2 * warp, w, sums, last ? own : nullptr);
         if (lane == 0) pieces[warp].head = 1, pieces[warp].head_ends = ends, pieces[warp].last_piece = last ? 0 : -1;
       } else if (!ends) {
-        put_piece<D, NT, INT8>(p, 2 * warp + 1, w, sums, own);
+        put_piece<D, NT>(p, 2 * warp + 1, w, sums, own);
         if (lane == 0) {
           Pieces& q = pieces[warp];
           q.tail = 1, q.last_piece = 1;
@@ -1190,10 +1190,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
           q.last = cut.holder(end + (part.s.pages - part.b) - 1);  // of its last unit
         }
       } else {
-        write_rows<D, NT, INT8>(p, part, group, w);
+        write_rows<D, NT>(p, part, group, w);
       }
     } else {
-      write_rows<D, NT, INT8>(p, part, group, w);
+      write_rows<D, NT>(p, part, group, w);
     }
   }
   if (dead) {  // a wait ran out: copies that are under way end before the CTA does

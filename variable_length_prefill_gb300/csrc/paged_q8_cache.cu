@@ -499,13 +499,8 @@ cudaError_t launch_move(const Q8MoveParams& p, bool write, cudaStream_t stream) 
   // n tokens touch at most n / 16 + 2 pages, and no more than n
   const long long pages = std::min<long long>(p.total_tokens, p.total_tokens / kPage + 2LL * p.c.num_seqs);
   const long long most = (pages * 2 * p.c.num_kv_heads + kMoveWarps - 1) / kMoveWarps;
-  if (write) {
-    const int grid = (int)std::min<long long>(most, p.c.sm_count * (D == 256 ? 2LL : 3LL));
-    return launch_behind(q8_write_kernel<D, FP16, INT8>, grid, p, stream);
-  } else {
-    const int grid = (int)std::min<long long>(most, p.c.sm_count * (D == 256 ? 2LL : 3LL));
-    return launch_behind(q8_read_kernel<D, FP16, INT8>, grid, p, stream);
-  }
+  const int grid = (int)std::min<long long>(most, p.c.sm_count * (D == 256 ? 2LL : 3LL));
+  return launch_behind(write ? q8_write_kernel<D, FP16, INT8> : q8_read_kernel<D, FP16, INT8>, grid, p, stream);
 }
 
 template <int D>
