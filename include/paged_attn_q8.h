@@ -27,6 +27,10 @@
  * never used as an address: its tokens are skipped, and attn_varlen_check on
  * the same stream returns ATTN_VARLEN_ERR_BAD_BLOCK_TABLE.  num_seqs == 0 or
  * total_tokens == 0 returns ATTN_VARLEN_OK and launches nothing.
+ *
+ * Of the operators of paged_attn_cache.h, paged_attn_cache_free, which moves no
+ * contents, works on these pages; write, accept, fork and compact take 16-bit
+ * caches only.
  */
 #ifndef PAGED_ATTN_Q8_H_
 #define PAGED_ATTN_Q8_H_
@@ -58,10 +62,13 @@ extern "C" {
  *
  * the page's scale becomes need, if the sequence has no tokens in the page
  * before the new ones; else the larger of need and its scale so far, rounded up
- * to a power of two (to 2^127, the largest there is, from above it).  New elements x become the code nearest to x / scale, ties
- * to even.  Where the scale changed, the codes of the page's earlier tokens are
- * rounded anew: the code nearest to code * (old scale / new scale), the largest
- * code where that is past it (under an old scale above 2^127 only).
+ * to a power of two (to 2^127, the largest there is, from above it).  New
+ * elements x become the code nearest to x / scale, ties to even.  Where the
+ * scale changed, the codes of the page's earlier tokens are rounded anew: the
+ * code nearest to code * (old scale / new scale), the largest code where that is
+ * past it (under an old scale above 2^127 only).  A scale that was raised stays
+ * raised: a draft that is rejected and written over later leaves its page's
+ * scale, and its earlier tokens' codes, as it made them.
  *
  * A non-finite element becomes NaN (e4m3), or -127, 0 or 127 for -infinity, NaN
  * and infinity (integers).  An old scale that is not finite and > 0 counts as
@@ -125,12 +132,13 @@ size_t paged_attn_q8_workspace_size(int head_size);
  *     w = softmax over p <= t of scale * query[row, h, :] . key_p.
  *
  * For decoding (n_i = 1) and a few new or drafted tokens; longer runs are right
- * too, but their contexts are read again for every 32 / (Hq / Hkv) tokens (16 /
- * (Hq / Hkv) for head_size 256).  What a row
- * does not see (later tokens, unused slots, pages with a bad id, positions below
- * 0 or past the table) has no part in it, whatever it holds.  A row that sees
- * nothing gets zeros.  A query row with a non-finite element gives NaN if it
- * sees anything.
+ * too, but their contexts are read again for every 8, 16, 24 or 32 rows (8 or 16
+ * for head_size 256) of tokens x Hq / Hkv, by what the batch's sequences have on
+ * average: a long run among many single tokens for every 8.  What a row does not
+ * see (later tokens, unused slots, pages with a bad id, positions below 0 or
+ * past the table) has no part in it, whatever it holds.  A row that sees nothing
+ * gets zeros.  A query row with a non-finite element gives NaN if it sees
+ * anything.
  *
  * Codes are exact operands of 16-bit products with sums in 32 bits.  A bf16
  * query row is taken as fp16 times a power of two, exact for elements above

@@ -42,11 +42,11 @@
 // launch joins what is then still open, at most two results of each CTA.
 //
 // Measured (captured calls; 32 query and 8 KV heads of 128, bf16, unless said): one token
-// on 64 contexts of 4096, 101 us with e4m3 codes (5.3 TB/s, 79 % of a copy's bandwidth)
-// and 96 with int8 ones, whose conversion is quicker; 128 contexts 186 us (85 %).  The
+// on 64 contexts of 4096, 100 us with e4m3 codes (5.4 TB/s, 79 % of a copy's bandwidth)
+// and 97 with int8 ones, whose conversion is quicker; 128 contexts 187 us (85 %).  The
 // start and the joins take about 12 us, and SMs differ in what they get from HBM by up
 // to a third, which equal ranges do not know.  3 contexts of up to 131072, 4 tokens
-// each, 40 query heads (20 rows): 150 us, bound by a page's chain of products and
+// each, 40 query heads (20 rows): 151 us, bound by a page's chain of products and
 // softmax at two warps a scheduler (2300 clocks for 24 rows, 450 for 8).  Four contexts of
 // 128: 7.3 us, latency.
 #include <cuda_fp16.h>
@@ -97,8 +97,8 @@ struct Cfg {
   static constexpr int JOIN = 4 * 3 * 2 * kTakers * ROWS;
   // Registers of a thread that computes and of one that copies, 256 of each; the 512
   // start with 128.  32 rows of O want all that the copying ones can spare (8 drafts
-  // of 4 heads on 64 contexts of 4096: 190 us with 224, 209 with 216), the others are
-  // held up by copying threads that spill (one token each: 99 us with 216, 107 with 224).
+  // of 4 heads on 64 contexts of 4096: 184 us with 224, 193 with 216), the others are
+  // held up by copying threads that spill (one token each: 99 us with 216, 106 with 224).
   static constexpr int TAKE_REGS = NT == 4 ? 224 : 216, COPY_REGS = 256 - TAKE_REGS;
   // query rows as operands stay in registers, or in shared memory where O needs those
   static constexpr bool KEPT = D * NT < 512;

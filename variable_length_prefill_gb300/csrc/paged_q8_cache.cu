@@ -293,10 +293,10 @@ __device__ __forceinline__ void write_few(const PageTask& k, const uint16_t* src
 // lane loads D / 32 elements of all 16 tokens and stores two rows of tokens, a
 // sector, at a time.
 //
-// Measured (captured calls): 12 prompts of up to 4195 tokens, 8 heads of 128, 38.8 us,
+// Measured (captured calls): 12 prompts of up to 4195 tokens, 8 heads of 128, 39.2 us,
 // 4.4 TB/s, 65 % of a copy's bandwidth: a warp has nothing in flight between its
 // loads and the next task's, at three CTAs an SM (two 44 us; four spill, 52).  One token
-// for each of 256 sequences, 16 heads of 128: 8.9 us, latency.  The walk over all
+// for each of 256 sequences, 16 heads of 128: 9.0 us, latency.  The walk over all
 // lengths costs the latter 2 us; without it (a CTA a sequence) a prompt among many
 // single tokens would have all of its pages to one CTA.
 // FULL: all 16 tokens of the page are new.
